@@ -46,6 +46,7 @@
  *   x, y          [R][T][H]       dtype     token rows, one slice per rank
  *   topk_ids      [R][T][k]       int32     expert ids from the router
  *   gates         [R][T][k]       float32   combine weights
+ *   (A2AV_MX8: x and recv hold 8-bit rows, expert_out and y bfloat16 ones)
  *   recv, expert_out [R][cap][H]  dtype     receive rows.  Source-major layout: rank d's
  *                                           rows from source s are rows recv_offsets[d][s]
  *                                           .. recv_offsets[d][s+1]-1 of slice d, sorted
@@ -78,6 +79,14 @@ typedef struct a2av_context* a2av_handle_t;
 /* element types of x, recv, expert_out and y */
 #define A2AV_F32  0
 #define A2AV_BF16 1
+#define A2AV_MX8  2   /* 8-bit rows: x and recv are rows of a2av_row_bytes(A2AV_MX8, H) bytes: H
+                         e4m3 elements, then one scale byte (E8M0: 2^(byte-127), 255 = NaN) for
+                         each 32 of them, then zeros up to a multiple of 16.  H is a multiple
+                         of 32.  expert_out and y are bfloat16. */
+/* element type of a2av_expert_matmul's weights only */
+#define A2AV_MX4  3   /* 4-bit elements (E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives),
+                         two a byte, the even one in the low half; scales as for A2AV_MX8, in
+                         an array of their own */
 
 /* return codes */
 #define A2AV_OK           0
@@ -90,6 +99,8 @@ typedef struct a2av_context* a2av_handle_t;
 /* device status bits, OR-ed into *status */
 #define A2AV_ST_EXPERT_RANGE  1u  /* an expert id was outside [0, E): that slot is dropped */
 #define A2AV_ST_RECV_OVERFLOW 2u  /* a rank received more rows than recv_capacity_rows */
+#define A2AV_ST_OFFSETS       8u  /* a2av_expert_matmul: a group start was negative or below the
+                                     one before it: that group is taken as empty */
 #define A2AV_ST_BOUNDS        4u  /* debug build only (liba2av_debug.so, compiled with
                                      A2AV_DEBUG=1): a device-side bounds check on a row
                                      index or a table value failed and that access was
@@ -116,7 +127,7 @@ typedef struct {
     int32_t num_ranks;          /* R, 1 .. 1024 */
     int32_t tokens_per_rank;    /* T, >= 0 */
     int32_t hidden;             /* H, >= 1 elements per row */
-    int32_t dtype;              /* A2AV_F32 or A2AV_BF16 */
+    int32_t dtype;              /* A2AV_F32, A2AV_BF16 or A2AV_MX8 */
     int32_t experts_per_rank;   /* E = R * experts_per_rank, 1 <= E <= 4096 */
     int32_t top_k;              /* k, 1 .. min(E, 64) */
     int64_t recv_capacity_rows; /* rows per rank's receive slice; 0 = worst case
@@ -240,12 +251,86 @@ int a2av_copy_recv_expert_offsets(a2av_handle_t h, int32_t* recv_expert_offsets,
  * [s][d] = first row of s's segment for d, [s][R] = rows s sent. */
 int a2av_copy_send_offsets(a2av_handle_t h, int32_t* send_offsets, void* stream);
 
+/* Where each local expert's rows start in the expert-major receive layout, as the device
+ * address of the handle's own table [R][epr+1]: what a2av_copy_recv_expert_offsets copies,
+ * without the copy.  The address stays the same for the handle's life; every dispatch
+ * rewrites the table in stream order.  Host-only: touches no GPU.  NULL unless the handle
+ * was created with A2AV_LAYOUT_EXPERT_MAJOR. */
+const int32_t* a2av_recv_expert_offsets(a2av_handle_t h);
+
+/* ---- the layer around the exchange: norm and experts ------------------------------- */
+
+/* Bytes of a row of n elements: 4n (A2AV_F32), 2n (A2AV_BF16), n + n/32 rounded up to a
+ * multiple of 16 (A2AV_MX8, n a multiple of 32); -1 for anything else.  Host-only. */
+int64_t a2av_row_bytes(int32_t dtype, int64_t n);
+
+/* Root-mean-square norm of each row, with the residual's addition before it:
+ *   s   = x + residual                       (s = x without one)
+ *   residual_out = round(s)
+ *   v   = s / sqrt(mean(s^2) + eps) * weight (float32; s is not rounded on the way)
+ *   y   = round(v)
+ *   y8  = v as A2AV_MX8 rows: the scale of 32 elements is the smallest power of two (at
+ *         least 2^-127) that keeps the largest of them within 448, every element is then
+ *         rounded to e4m3 (nearest, ties to even).  32 elements of which one is infinite
+ *         or NaN get the scale NaN.
+ * x, residual, residual_out, y (device) [rows][hidden] dtype (A2AV_F32 or A2AV_BF16);
+ * weight (device) [hidden] dtype, NULL = ones; y8 (device) [rows][a2av_row_bytes(A2AV_MX8,
+ * hidden)], 16-byte aligned, hidden a multiple of 32.  residual may be NULL; of residual_out
+ * (only with residual), y and y8 at least one is given.  1 <= hidden <= 65536.  Squares are
+ * summed in float32: a row with an element past 1e19 comes out as zeros or NaN.
+ * residual_out and y may be x or residual themselves (every row is read before any of it is
+ * written); beyond that no output may overlap another array.  No workspace; it can be
+ * captured in a hipGraph.  Errors: A2AV_ERR_INVALID, A2AV_ERR_HIP. */
+int a2av_rmsnorm(const void* x, const void* residual, const void* weight, void* residual_out, void* y, void* y8,
+                 int64_t rows, int32_t hidden, int32_t dtype, float eps, void* stream);
+
+/* activations of a2av_expert_matmul */
+#define A2AV_ACT_NONE   0
+#define A2AV_ACT_SWIGLU 1   /* silu(g) * u, g from the first n/2 rows of the weight, u from the
+                               others: n/2 columns come out */
+
+typedef struct {
+    int32_t num_ranks;          /* R >= 1 */
+    int32_t experts_per_rank;   /* R * experts_per_rank <= 4096 */
+    int64_t capacity_rows;      /* rows of each rank's slice of in and out, 0 .. 2^31 - 1 */
+    int32_t k;                  /* elements of an input row, 1 .. 2^20 */
+    int32_t n;                  /* rows of an expert's weight, 1 .. 2^20 */
+    int32_t in_dtype;           /* A2AV_F32, A2AV_BF16 or A2AV_MX8 */
+    int32_t weight_dtype;       /* in A2AV_F32: A2AV_F32; in A2AV_BF16: A2AV_BF16 or A2AV_MX4;
+                                   in A2AV_MX8: A2AV_MX8 or A2AV_MX4 */
+    int32_t out_dtype;          /* in A2AV_F32: A2AV_F32; in A2AV_BF16: A2AV_BF16; in A2AV_MX8:
+                                   A2AV_BF16 or A2AV_MX8 */
+    int32_t activation;         /* A2AV_ACT_NONE or A2AV_ACT_SWIGLU */
+} a2av_matmul_t;
+
+/* The experts' matrix products on expert-major receive rows, all experts in one call, their
+ * row counts read on the GPU:
+ *   out[d][r][i] = round( act( sum_j in[d][r][j] * weight[e][i][j] ) )
+ * for every row r of rank d's slice in [expert_offsets[d][le], expert_offsets[d][le + 1]),
+ * e = d * experts_per_rank + le.  Sums and the activation are in float32 (products of 4- and
+ * 8-bit elements are exact), rounded once to out_dtype (A2AV_MX8 as a2av_rmsnorm's y8).
+ * Rows in no group, and rows at or past the capacity, are neither read nor written.
+ * in  (device) [R][capacity][a2av_row_bytes(in_dtype, k)];
+ * expert_offsets (device) [R][experts_per_rank + 1], as a2av_copy_recv_expert_offsets gives
+ *     it (or the handle's own table, a2av_recv_expert_offsets): read when the kernels run.  A
+ *     start that is negative or below the one before it sets A2AV_ST_OFFSETS and the group
+ *     that begins or ends so is empty; rows that two groups then share hold either's result;
+ * weight (device) [R * experts_per_rank][n][k] of weight_dtype (A2AV_MX4: k/2 bytes a row);
+ * weight_scales (device) [R * experts_per_rank][n][k/32] scale bytes for A2AV_MX8 and A2AV_MX4
+ *     (k a multiple of 32), NULL otherwise;
+ * out (device) [R][capacity][a2av_row_bytes(out_dtype, n or n/2)]; it may overlap no other
+ *     array.  status (device) is OR-ed.
+ * 8-bit rows and 4- and 8-bit weights are 16-byte aligned.  No workspace; it can be captured
+ * in a hipGraph.  Errors: A2AV_ERR_INVALID, A2AV_ERR_HIP. */
+int a2av_expert_matmul(const a2av_matmul_t* cfg, const void* in, const int32_t* expert_offsets, const void* weight,
+                       const void* weight_scales, void* out, uint32_t* status, void* stream);
+
 /* ---- harness calls (stand-ins for the model around the collective) ---------------- */
 
 /* Expert stand-in over the received rows of the latest dispatch: for every received
  * row, out = in (A2AV_EXPERT_IDENTITY) or round(in * (1 + e/256)) in float32 with one
  * rounding to dtype (A2AV_EXPERT_SCALE), e being the row's expert.  in, out (device)
- * [R][cap][H]; in == out is allowed. */
+ * [R][cap][H]; in == out is allowed.  Not for A2AV_MX8 handles (A2AV_ERR_INVALID). */
 int a2av_expert_apply(a2av_handle_t h, const void* in, void* out, int32_t mode, void* stream);
 
 /* Router stand-in for replayed decode steps: copies step (*counter % steps) of the

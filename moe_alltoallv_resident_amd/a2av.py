@@ -5,6 +5,7 @@ raw device addresses as ints) where the C call takes device pointers; the stream
 defaults to torch's current stream.  No step of the path runs in Python: the library is
 required, and a missing build raises at import of the first call.
 """
+import contextlib
 import ctypes
 import os
 
@@ -12,6 +13,8 @@ import torch
 
 F32 = 0
 BF16 = 1
+MX8 = 2
+MX4 = 3
 OK = 0
 ERR_INVALID = -1
 ERR_NOMEM = -2
@@ -22,6 +25,9 @@ NOALLOC_SCRATCH_BYTES = 1 << 20
 ST_EXPERT_RANGE = 1
 ST_RECV_OVERFLOW = 2
 ST_BOUNDS = 4
+ST_OFFSETS = 8
+ACT_NONE = 0
+ACT_SWIGLU = 1
 EXPERT_IDENTITY = 0
 EXPERT_SCALE = 1
 PATH_STAGED = 0
@@ -40,10 +46,12 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
                         "liba2av_debug.so" if os.environ.get("A2AV_DEBUG") == "1" else "liba2av.so")
 EXPORTS = ("a2av_create", "a2av_destroy", "a2av_workspace_bytes", "a2av_dispatch", "a2av_combine",
            "a2av_alltoallv", "a2av_alltoallv_noalloc", "a2av_copy_positions", "a2av_copy_recv_expert_offsets",
-           "a2av_copy_send_offsets", "a2av_expert_apply", "a2av_route_step", "a2av_copy_reference",
+           "a2av_copy_send_offsets", "a2av_recv_expert_offsets", "a2av_row_bytes", "a2av_rmsnorm",
+           "a2av_expert_matmul", "a2av_expert_apply", "a2av_route_step", "a2av_copy_reference",
            "a2av_stream_reference", "a2av_timing_begin", "a2av_timing_end", "a2av_error_string")
 
-TORCH_DTYPE = {F32: torch.float32, BF16: torch.bfloat16}
+# 8-bit rows and 4- and 8-bit weights are bytes
+TORCH_DTYPE = {F32: torch.float32, BF16: torch.bfloat16, MX8: torch.uint8, MX4: torch.uint8}
 
 
 class Config(ctypes.Structure):
@@ -51,6 +59,13 @@ class Config(ctypes.Structure):
                 ("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("experts_per_rank", ctypes.c_int32), ("top_k", ctypes.c_int32),
                 ("recv_capacity_rows", ctypes.c_int64), ("path", ctypes.c_int32), ("recv_layout", ctypes.c_int32)]
+
+
+class Matmul(ctypes.Structure):
+    _fields_ = [("num_ranks", ctypes.c_int32), ("experts_per_rank", ctypes.c_int32),
+                ("capacity_rows", ctypes.c_int64), ("k", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("in_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32)]
 
 
 class A2AVError(RuntimeError):
@@ -82,6 +97,12 @@ def lib():
         L.a2av_copy_positions.argtypes = [vp, vp, vp]
         L.a2av_copy_send_offsets.argtypes = [vp, vp, vp]
         L.a2av_copy_recv_expert_offsets.argtypes = [vp, vp, vp]
+        L.a2av_recv_expert_offsets.argtypes = [vp]
+        L.a2av_recv_expert_offsets.restype = vp
+        L.a2av_row_bytes.argtypes = [i32, i64]
+        L.a2av_row_bytes.restype = i64
+        L.a2av_rmsnorm.argtypes = [vp] * 6 + [i64, i32, i32, ctypes.c_float, vp]
+        L.a2av_expert_matmul.argtypes = [ctypes.POINTER(Matmul)] + [vp] * 7
         L.a2av_expert_apply.argtypes = [vp, vp, vp, i32, vp]
         L.a2av_route_step.argtypes = [vp, vp, i32, i64, vp, vp, vp, vp]
         L.a2av_copy_reference.argtypes = [vp, vp, i64, i64, vp]
@@ -91,7 +112,7 @@ def lib():
         L.a2av_error_string.argtypes = [ctypes.c_int]
         L.a2av_error_string.restype = ctypes.c_char_p
         for f in EXPORTS:
-            if f not in ("a2av_workspace_bytes", "a2av_error_string"):
+            if f not in ("a2av_workspace_bytes", "a2av_error_string", "a2av_recv_expert_offsets", "a2av_row_bytes"):
                 getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -181,6 +202,26 @@ def a2av_copy_send_offsets(h, send_offsets, stream=None) -> None:
     _check("a2av_copy_send_offsets", lib().a2av_copy_send_offsets(h, _ptr(send_offsets), _stream(stream)))
 
 
+def a2av_recv_expert_offsets(h) -> int:
+    """Device address of the handle's own table of group starts (expert-major handles)."""
+    return lib().a2av_recv_expert_offsets(h)
+
+
+def a2av_row_bytes(dtype: int, n: int) -> int:
+    return lib().a2av_row_bytes(dtype, n)
+
+
+def a2av_rmsnorm(x, residual, weight, residual_out, y, y8, rows, hidden, dtype, eps, stream=None) -> None:
+    _check("a2av_rmsnorm", lib().a2av_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y),
+                                              _ptr(y8), rows, hidden, dtype, eps, _stream(stream)))
+
+
+def a2av_expert_matmul(cfg: Matmul, inp, expert_offsets, weight, weight_scales, out, status, stream=None) -> None:
+    _check("a2av_expert_matmul",
+           lib().a2av_expert_matmul(ctypes.byref(cfg), _ptr(inp), _ptr(expert_offsets), _ptr(weight),
+                                    _ptr(weight_scales), _ptr(out), _ptr(status), _stream(stream)))
+
+
 def a2av_expert_apply(h, inp, out, mode, stream=None) -> None:
     _check("a2av_expert_apply", lib().a2av_expert_apply(h, _ptr(inp), _ptr(out), mode, _stream(stream)))
 
@@ -221,10 +262,103 @@ def a2av_timing_end(h):
     return list(ms), list(n)
 
 
+def _same_device(named):
+    # host-side checks only, as Session's: every tensor a contiguous GPU tensor of one device
+    device = None
+    for name, t in named:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous GPU tensor")
+        if device is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+        device = t.device
+    return device
+
+
+def _need(name, t, dtype, shape):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _on(device):
+    # the library launches on the current GPU
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, y8=None, stream=None) -> None:
+    """a2av_rmsnorm on torch tensors, with their types and sizes checked.
+
+    x [..., hidden] float32 or bfloat16 (weight, residual, residual_out, y alike); y8 uint8
+    [..., a2av_row_bytes(MX8, hidden)].  weight may be None (ones).  The outputs given are
+    written; at least one is.
+    """
+    device = _same_device((("x", x), ("weight", weight), ("residual", residual), ("residual_out", residual_out),
+                           ("y", y), ("y8", y8)))
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"x has dtype {x.dtype}, expected float32 or bfloat16")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    hidden = x.shape[-1]
+    if weight is not None:
+        _need("weight", weight, x.dtype, (hidden,))
+    for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
+        if t is not None:
+            _need(name, t, x.dtype, x.shape)
+    if y8 is not None:
+        _need("y8", y8, torch.uint8, x.shape[:-1] + (a2av_row_bytes(MX8, hidden),))
+    rows = x.numel() // hidden if hidden else 0
+    with _on(device):
+        a2av_rmsnorm(x, residual, weight, residual_out, y, y8, rows, hidden,
+                     F32 if x.dtype == torch.float32 else BF16, eps, stream)
+
+
+def _matmul_config(R, epr, cap, inp, weight, out, weight_scales, in_dtype, weight_dtype, out_dtype, activation) -> Matmul:
+    for name, d in (("in_dtype", in_dtype), ("weight_dtype", weight_dtype), ("out_dtype", out_dtype)):
+        if d not in TORCH_DTYPE or (d == MX4 and name != "weight_dtype"):
+            raise ValueError(f"{name} {d} is not an element type of this argument")
+    if weight.dim() != 3:
+        raise ValueError(f"weight has {weight.dim()} dimensions, expected 3")
+    n, k = weight.shape[1], weight.shape[2] * (2 if weight_dtype == MX4 else 1)
+    width = n // 2 if activation == ACT_SWIGLU else n
+    _need("weight", weight, TORCH_DTYPE[weight_dtype], (R * epr, n, weight.shape[2]))
+    _need("inp", inp, TORCH_DTYPE[in_dtype], (R, cap, a2av_row_bytes(MX8, k) if in_dtype == MX8 else k))
+    _need("out", out, TORCH_DTYPE[out_dtype], (R, cap, a2av_row_bytes(MX8, width) if out_dtype == MX8 else width))
+    if weight_scales is not None:
+        _need("weight_scales", weight_scales, torch.uint8, (R * epr, n, k // 32))
+    return Matmul(R, epr, cap, k, n, in_dtype, weight_dtype, out_dtype, activation)
+
+
+def expert_matmul(inp, expert_offsets, weight, out, status, weight_scales=None, in_dtype=BF16, weight_dtype=BF16,
+                  out_dtype=BF16, activation=ACT_NONE, stream=None) -> None:
+    """a2av_expert_matmul on torch tensors, with their types and sizes checked.
+
+    inp [R][cap][row] and out [R][cap][row] (MX8: uint8 rows of a2av_row_bytes);
+    expert_offsets int32 [R][epr + 1]; weight [R * epr][n][k] (MX4: uint8 [..][k / 2]; MX8:
+    uint8); weight_scales uint8 [R * epr][n][k / 32] for MX4 and MX8; status int32 [1].
+    """
+    device = _same_device((("inp", inp), ("expert_offsets", expert_offsets), ("weight", weight), ("out", out),
+                           ("status", status), ("weight_scales", weight_scales)))
+    if expert_offsets.dim() != 2 or inp.dim() != 3:
+        raise ValueError("expert_offsets must be [R][epr + 1] and inp [R][cap][row]")
+    _need("expert_offsets", expert_offsets, torch.int32, (inp.shape[0], expert_offsets.shape[1]))
+    cfg = _matmul_config(inp.shape[0], expert_offsets.shape[1] - 1, inp.shape[1], inp, weight, out, weight_scales,
+                         in_dtype, weight_dtype, out_dtype, activation)
+    if status.dtype != torch.int32 or status.numel() < 1:
+        raise TypeError("status must be an int32 tensor of one element")
+    with _on(device):
+        a2av_expert_matmul(cfg, inp, expert_offsets, weight, weight_scales, out, status, stream)
+
+
 class Session:
     """A handle plus the caller-owned device buffers of one configuration.
 
-    Allocates (once) recv [R][cap][H], split [R][E], recv_counts [R][R],
+    dtype MX8: x and recv are 8-bit rows [..][a2av_row_bytes(MX8, H)] (uint8), the experts'
+    outputs and y bfloat16.  Allocates (once) recv [R][cap][H], split [R][E], recv_counts [R][R],
     recv_offsets [R][R+1] and status on the current GPU; dispatch/combine then only
     enqueue library calls, so they can be captured in a graph.
     """
@@ -241,11 +375,14 @@ class Session:
         self.cap = recv_capacity_rows or num_ranks * tokens_per_rank * min(top_k, experts_per_rank)
         self.dtype = dtype
         self.torch_dtype = TORCH_DTYPE[dtype]
+        # columns of a dispatched row, element type of a combined one
+        self.cols = a2av_row_bytes(MX8, hidden) if dtype == MX8 else hidden
+        self.out_dtype = torch.bfloat16 if dtype == MX8 else self.torch_dtype
         self.device = torch.device(device)
         with torch.cuda.device(self.device):
             self.handle = a2av_create(self.cfg)
         R = num_ranks
-        self.recv = torch.empty((R, self.cap, hidden), dtype=self.torch_dtype, device=self.device)
+        self.recv = torch.empty((R, self.cap, self.cols), dtype=self.torch_dtype, device=self.device)
         self.split = torch.empty((R, self.E), dtype=torch.int32, device=self.device)
         self.recv_counts = torch.empty((R, R), dtype=torch.int32, device=self.device)
         self.recv_offsets = torch.empty((R, R + 1), dtype=torch.int32, device=self.device)
@@ -264,8 +401,8 @@ class Session:
             raise ValueError(f"{name} is on {t.device}, the session on {self.device}")
 
     def dispatch(self, x, topk_ids, stream=None):
-        R, T, H, k = self.R, self.T, self.H, self.k
-        self._check_tensor("x", x, self.torch_dtype, R * T * H)
+        R, T, k = self.R, self.T, self.k
+        self._check_tensor("x", x, self.torch_dtype, R * T * self.cols)
         self._check_tensor("topk_ids", topk_ids, torch.int32, R * T * k)
         a2av_dispatch(self.handle, x, topk_ids, self.recv, self.split, self.recv_counts, self.recv_offsets,
                       self.status, stream)
@@ -280,11 +417,27 @@ class Session:
 
     def combine(self, expert_out, gates, y, stream=None):
         R, T, H, k = self.R, self.T, self.H, self.k
-        self._check_tensor("expert_out", expert_out, self.torch_dtype, R * self.cap * H)
+        self._check_tensor("expert_out", expert_out, self.out_dtype, R * self.cap * H)
         self._check_tensor("gates", gates, torch.float32, R * T * k)
-        self._check_tensor("y", y, self.torch_dtype, R * T * H)
+        self._check_tensor("y", y, self.out_dtype, R * T * H)
         a2av_combine(self.handle, expert_out, gates, y, self.status, stream)
         return y
+
+    def expert_matmul(self, inp, weight, out, weight_scales=None, in_dtype=None, weight_dtype=BF16, out_dtype=BF16,
+                      activation=ACT_NONE, stream=None):
+        """The experts' products on rows of the latest dispatch (expert-major sessions): inp and out are
+        [R][cap][row], the group starts are the handle's own table."""
+        in_dtype = self.dtype if in_dtype is None else in_dtype
+        if self.recv_layout != LAYOUT_EXPERT_MAJOR:
+            raise ValueError("expert_matmul needs an expert-major session")
+        device = _same_device((("inp", inp), ("weight", weight), ("out", out), ("weight_scales", weight_scales),
+                               ("status", self.status)))
+        cfg = _matmul_config(self.R, self.epr, self.cap, inp, weight, out, weight_scales, in_dtype, weight_dtype,
+                             out_dtype, activation)
+        with _on(device):
+            a2av_expert_matmul(cfg, inp, a2av_recv_expert_offsets(self.handle), weight, weight_scales, out, self.status,
+                               stream)
+        return out
 
     def positions(self):
         pos = torch.empty((self.R, self.T, self.k), dtype=torch.int32, device=self.device)

@@ -19,7 +19,8 @@ struct TimedLaunch {
 
 struct a2av_context {
     a2av_config_t cfg;
-    Shape sh;
+    Shape sh;             // rows as dispatched
+    Shape out;            // rows as combined: the same but for 8-bit rows, combined in bfloat16
     int device;
     bool direct;          // A2AV_PATH_DIRECT: no send buffer, rows go straight to receivers
     void* send_buf;       // [R][T*k][row]: send segments, then the return buffer (staged)
@@ -47,7 +48,8 @@ bool make_shape(const a2av_config_t* c, Shape* sh) {
     if (!c) return false;
     if (c->num_ranks < 1 || c->num_ranks > a2av::kMaxRanks) return false;
     if (c->tokens_per_rank < 0 || c->hidden < 1) return false;
-    if (c->dtype != A2AV_F32 && c->dtype != A2AV_BF16) return false;
+    if (c->dtype != A2AV_F32 && c->dtype != A2AV_BF16 && c->dtype != A2AV_MX8) return false;
+    if (c->dtype == A2AV_MX8 && c->hidden % 32 != 0) return false;
     if (c->experts_per_rank < 1) return false;
     const int64_t E = (int64_t)c->num_ranks * c->experts_per_rank;
     if (E > a2av::kMaxExperts) return false;
@@ -71,7 +73,7 @@ bool make_shape(const a2av_config_t* c, Shape* sh) {
     sh->nbits = nbits_for((int32_t)E);
     sh->TK = TK;
     sh->cap = cap;
-    sh->row_bytes = (int64_t)c->hidden * (c->dtype == A2AV_BF16 ? 2 : 4);
+    sh->row_bytes = a2av_row_bytes(c->dtype, c->hidden);
     sh->num_cu = 256;
     sh->layout = c->recv_layout;
     return true;
@@ -98,9 +100,20 @@ MetaLayout meta_layout(const Shape& sh) {
     return m;
 }
 
+// Rows as combined: 8-bit rows come back from the experts in bfloat16.
+Shape combined_shape(const Shape& sh) {
+    Shape out = sh;
+    if (sh.dtype == A2AV_MX8) {
+        out.dtype = A2AV_BF16;
+        out.row_bytes = (int64_t)sh.H * 2;
+    }
+    return out;
+}
+
+// The send buffer holds the dispatched rows first and the returned ones afterwards.
 size_t send_bytes(const a2av_config_t* c, const Shape& sh) {
     if (c->path == A2AV_PATH_DIRECT) return 0;
-    return (size_t)sh.R * (size_t)sh.TK * (size_t)sh.row_bytes;
+    return (size_t)sh.R * (size_t)sh.TK * (size_t)std::max(sh.row_bytes, combined_shape(sh).row_bytes);
 }
 
 bool on_device(const a2av_context* h) {
@@ -238,6 +251,7 @@ int a2av_create(const a2av_config_t* cfg, a2av_handle_t* out) {
         delete h;
         return A2AV_ERR_HIP;
     }
+    h->out = combined_shape(h->sh);
     const MetaLayout m = meta_layout(sh);
     const size_t sb = std::max<size_t>(send_bytes(cfg, sh), kAlign);
     if (hipMalloc(&h->send_buf, sb) != hipSuccess) { (void)hipGetLastError(); delete h; return A2AV_ERR_NOMEM; }
@@ -323,7 +337,7 @@ int a2av_dispatch(a2av_handle_t h, const void* x, const int32_t* topk_ids, void*
 int a2av_combine(a2av_handle_t h, const void* expert_out, const float* gates, void* y, uint32_t* status,
                  void* stream) {
     if (!h || !status_ok(status) || !on_device(h) || !h->routed) return A2AV_ERR_INVALID;
-    const Shape& sh = h->sh;
+    const Shape& sh = h->out;
     if (has_tokens(sh) && (!gates || !y || (sh.cap > 0 && !expert_out))) return A2AV_ERR_INVALID;
     const void* ptrs[] = {expert_out, y, h->send_buf};
     const int vec = a2av::pick_vec_bytes(sh.row_bytes, ptrs, 3);
@@ -411,6 +425,10 @@ int a2av_copy_recv_expert_offsets(a2av_handle_t h, int32_t* recv_expert_offsets,
                           static_cast<hipStream_t>(stream)) == hipSuccess ? A2AV_OK : A2AV_ERR_HIP;
 }
 
+const int32_t* a2av_recv_expert_offsets(a2av_handle_t h) {
+    return h && h->sh.layout == A2AV_LAYOUT_EXPERT_MAJOR ? h->tb.recv_eoff : nullptr;
+}
+
 int a2av_copy_send_offsets(a2av_handle_t h, int32_t* send_offsets, void* stream) {
     if (!h || !send_offsets || !on_device(h)) return A2AV_ERR_INVALID;
     const size_t n = sizeof(int32_t) * (size_t)h->sh.R * (h->sh.R + 1);
@@ -422,6 +440,7 @@ int a2av_expert_apply(a2av_handle_t h, const void* in, void* out, int32_t mode, 
     if (!h || !on_device(h) || !h->routed) return A2AV_ERR_INVALID;
     if (mode != A2AV_EXPERT_IDENTITY && mode != A2AV_EXPERT_SCALE) return A2AV_ERR_INVALID;
     const Shape& sh = h->sh;
+    if (sh.dtype == A2AV_MX8) return A2AV_ERR_INVALID;
     if (has_tokens(sh) && sh.cap > 0 && (!in || !out)) return A2AV_ERR_INVALID;
     const void* ptrs[] = {in, out};
     const int vec = a2av::pick_vec_bytes(sh.row_bytes, ptrs, 2);

@@ -1,0 +1,296 @@
+// The experts' matrix products on expert-major receive rows (declared in include/a2av.h):
+// out[r] = act(in[r] . weight_e^T) for every row r of every expert e, with the row counts
+// read on the GPU.
+//
+// No host knows how many rows an expert got, so no grid can be cut to them: every block
+// reads the group starts, counts the row tiles of every expert into LDS and walks the tile
+// list (tile t, t + blocks, ...) until it ends.
+#include "../../include/a2av.h"
+#include "a2av_internal.h"
+#include "a2av_mx.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace a2av {
+namespace {
+
+constexpr int kWave = 64;
+constexpr int32_t kMaxDim = 1 << 20;
+constexpr uint32_t kStOffsets = 8u;
+static_assert(kStOffsets == A2AV_ST_OFFSETS, "status bit");
+
+struct ExpertArgs {
+    const uint8_t* in;
+    const int32_t* off;      // [R][epr + 1]
+    const uint8_t* weight;
+    const uint8_t* scales;
+    uint8_t* out;
+    uint32_t* status;
+    int64_t cap;
+    int64_t in_row;          // bytes of a row of in, weight and out
+    int64_t w_row;
+    int64_t out_row;
+    int32_t R, epr, G;       // G = R * epr groups
+    int32_t K, N;
+    int32_t width;           // columns that come out
+    int32_t in_dtype, w_dtype, out_dtype;
+    int32_t swiglu;
+};
+
+struct Group {
+    int64_t row;             // first row, counted over all slices
+    int32_t rows;
+};
+
+// Group g's rows: starts past the capacity are cut to it (a receive overflow), a start out
+// of order leaves the group empty.
+__device__ inline Group group_of(const ExpertArgs& a, int g, bool* bad) {
+    const int d = g / a.epr, le = g - d * a.epr;
+    const int32_t* p = a.off + (int64_t)d * (a.epr + 1) + le;
+    int32_t b = p[0], e = p[1];
+    if (b < 0 || e < b) {
+        *bad = true;
+        b = e = 0;
+    }
+    const int32_t cap = (int32_t)a.cap;
+    b = min(b, cap);
+    e = min(e, cap);
+    return Group{(int64_t)d * a.cap + b, e - b};
+}
+
+// Row tiles of every group, as ends[g] = tiles of groups 0 .. g; returns how many there are.
+// Every thread of the block calls it; `tiles(rows)` says how many tiles a group has.
+template <int THREADS, typename F>
+__device__ int count_tiles(const ExpertArgs& a, int* ends, int* wave_sum, F&& tiles) {
+    const int per = (a.G + THREADS - 1) / THREADS;
+    const int g0 = threadIdx.x * per;
+    int sum = 0;
+    bool bad = false;
+    for (int i = 0; i < per; ++i) {
+        if (g0 + i >= a.G) break;
+        sum += tiles(group_of(a, g0 + i, &bad).rows);
+        ends[g0 + i] = sum;
+    }
+    if (bad && blockIdx.x == 0) atomicOr(a.status, kStOffsets);
+    int scan = sum;
+#pragma unroll
+    for (int m = 1; m < kWave; m <<= 1) {
+        const int up = __shfl_up(scan, m);
+        if ((int)(threadIdx.x % kWave) >= m) scan += up;
+    }
+    if (threadIdx.x % kWave == kWave - 1) wave_sum[threadIdx.x / kWave] = scan;
+    __syncthreads();
+    int before = scan - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / kWave; ++w) {
+        const int v = wave_sum[w];
+        if (w < (int)threadIdx.x / kWave) before += v;
+        total += v;
+    }
+    for (int i = 0; i < per; ++i) {
+        if (g0 + i >= a.G) break;
+        ends[g0 + i] += before;
+    }
+    __syncthreads();
+    return total;
+}
+
+// The group of row tile t: the first whose end is past t.
+__device__ inline int find_group(const int* ends, int G, int t) {
+    int lo = 0, hi = G - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (ends[mid] > t) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+__device__ inline float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+
+// ---- the general form ----------------------------------------------------------------
+// Any width, stride and alignment that the call allows: elements are read one by one,
+// widened to float32 and multiplied on the vector units.
+
+__device__ inline float load_in(const ExpertArgs& a, const uint8_t* row, int k) {
+    if (a.in_dtype == A2AV_F32) return ((const float*)row)[k];
+    if (a.in_dtype == A2AV_BF16) return bf16_to_f32(((const u16*)row)[k]);
+    return e4m3_to_f32(row[k]) * mx_scale(row[a.K + k / kMxGroup]);
+}
+
+__device__ inline float load_weight(const ExpertArgs& a, int64_t row, int k) {
+    const uint8_t* p = a.weight + row * a.w_row;
+    if (a.w_dtype == A2AV_F32) return ((const float*)p)[k];
+    if (a.w_dtype == A2AV_BF16) return bf16_to_f32(((const u16*)p)[k]);
+    const float s = mx_scale(a.scales[row * (a.K / kMxGroup) + k / kMxGroup]);
+    if (a.w_dtype == A2AV_MX8) return e4m3_to_f32(p[k]) * s;
+    return e2m1_to_f32((p[k / 2] >> (k % 2 * 4)) & 15u) * s;
+}
+
+constexpr int kGenThreads = 256;
+constexpr int kGenM = 32, kGenN = 64, kGenK = 32;   // rows, weight rows and elements of a step
+
+__global__ void __launch_bounds__(kGenThreads) expert_general_kernel(ExpertArgs a) {
+    __shared__ int ends[kMaxExperts];
+    __shared__ int wave_sum[kGenThreads / kWave];
+    __shared__ float xs[kGenM][kGenK + 1];
+    __shared__ float ws[kGenN][kGenK + 1];
+    __shared__ float res[kGenM][kGenN + 1];
+    const int mt = count_tiles<kGenThreads>(a, ends, wave_sum, [](int rows) { return (rows + kGenM - 1) / kGenM; });
+    const int cols = a.swiglu ? kGenN / 2 : kGenN;       // output columns of a tile
+    const int nt = (a.width + cols - 1) / cols;
+    const int tm = threadIdx.x / 16 * 2, tn = threadIdx.x % 16 * 4;
+    for (int64_t t = blockIdx.x; t < (int64_t)mt * nt; t += gridDim.x) {
+        const int t_m = (int)(t / nt), col0 = (int)(t % nt) * cols;
+        const int g = find_group(ends, a.G, t_m);
+        bool bad = false;
+        const Group grp = group_of(a, g, &bad);
+        const int m0 = (t_m - (g ? ends[g - 1] : 0)) * kGenM;
+        const int rows = min(kGenM, grp.rows - m0);
+        const uint8_t* in = a.in + (grp.row + m0) * a.in_row;
+        uint8_t* out = a.out + (grp.row + m0) * a.out_row;
+        const int width = min(cols, a.width - col0);
+        float acc[2][4] = {};
+        for (int k0 = 0; k0 < a.K; k0 += kGenK) {
+            for (int i = threadIdx.x; i < kGenM * kGenK; i += kGenThreads) {
+                const int r = i / kGenK, k = k0 + i % kGenK;
+                xs[r][i % kGenK] = r < rows && k < a.K ? load_in(a, in + r * a.in_row, k) : 0.0f;
+            }
+            for (int i = threadIdx.x; i < kGenN * kGenK; i += kGenThreads) {
+                // with SwiGLU weight rows come in pairs: tile row 2c is column c's gate, 2c + 1 its up
+                const int r = i / kGenK, k = k0 + i % kGenK;
+                const int c = a.swiglu ? r / 2 : r;
+                const int64_t wr = (int64_t)g * a.N + col0 + c + (a.swiglu && r % 2 ? a.width : 0);
+                ws[r][i % kGenK] = c < width && k < a.K ? load_weight(a, wr, k) : 0.0f;
+            }
+            __syncthreads();
+#pragma unroll 8
+            for (int k = 0; k < kGenK; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[tm + i][k], ws[tn + j][k], acc[i][j]);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (a.swiglu) {
+                    if (j % 2 == 0) res[tm + i][(tn + j) / 2] = silu_mul(acc[i][j], acc[i][j + 1]);
+                } else {
+                    res[tm + i][tn + j] = acc[i][j];
+                }
+            }
+        __syncthreads();
+        if (a.out_dtype != A2AV_MX8) {
+            for (int i = threadIdx.x; i < kGenM * kGenN; i += kGenThreads) {
+                const int r = i / kGenN, c = i % kGenN;
+                if (r >= rows || c >= width) continue;
+                uint8_t* p = out + r * a.out_row;
+                if (a.out_dtype == A2AV_F32) ((float*)p)[col0 + c] = res[r][c];
+                else ((u16*)p)[col0 + c] = (u16)f32_to_bf16(res[r][c]);
+            }
+        } else {
+            // width is a multiple of 32, so is every tile's: one thread a scale
+            const int groups = width / kMxGroup;
+            for (int i = threadIdx.x; i < rows * groups; i += kGenThreads) {
+                const int r = i / groups, c0 = i % groups * kMxGroup;
+                uint32_t m = 0;
+                for (int c = 0; c < kMxGroup; ++c) m = max(m, abs_bits(res[r][c0 + c]));
+                const uint32_t sb = mx_scale_byte(m);
+                const float f = mx_inverse(sb);
+                uint8_t* p = out + r * a.out_row;
+                for (int c = 0; c < kMxGroup; c += 4)
+                    *(uint32_t*)(p + col0 + c0 + c) = mx8_pack(res[r][c0 + c] * f, res[r][c0 + c + 1] * f,
+                                                               res[r][c0 + c + 2] * f, res[r][c0 + c + 3] * f, sb == 255u);
+                p[a.width + (col0 + c0) / kMxGroup] = (uint8_t)sb;
+            }
+            const int used = a.width + a.width / kMxGroup, pad = (int)a.out_row - used;
+            if (col0 + width == a.width)
+                for (int i = threadIdx.x; i < rows * pad; i += kGenThreads) out[i / pad * a.out_row + used + i % pad] = 0;
+        }
+        __syncthreads();
+    }
+}
+
+bool make_args(const a2av_matmul_t* c, ExpertArgs* a) {
+    if (!c || c->num_ranks < 1 || c->experts_per_rank < 1) return false;
+    if ((int64_t)c->num_ranks * c->experts_per_rank > kMaxExperts) return false;
+    if (c->capacity_rows < 0 || c->capacity_rows > INT32_MAX) return false;
+    if (c->k < 1 || c->k > kMaxDim || c->n < 1 || c->n > kMaxDim) return false;
+    const int32_t i = c->in_dtype, w = c->weight_dtype, o = c->out_dtype;
+    const bool types = (i == A2AV_F32 && w == A2AV_F32 && o == A2AV_F32) ||
+                       (i == A2AV_BF16 && (w == A2AV_BF16 || w == A2AV_MX4) && o == A2AV_BF16) ||
+                       (i == A2AV_MX8 && (w == A2AV_MX8 || w == A2AV_MX4) && (o == A2AV_BF16 || o == A2AV_MX8));
+    if (!types || (c->activation != A2AV_ACT_NONE && c->activation != A2AV_ACT_SWIGLU)) return false;
+    const bool mx = w == A2AV_MX8 || w == A2AV_MX4;
+    if (mx && c->k % kMxGroup != 0) return false;
+    if (c->activation == A2AV_ACT_SWIGLU && c->n % 2 != 0) return false;
+    const int32_t width = c->activation == A2AV_ACT_SWIGLU ? c->n / 2 : c->n;
+    if (o == A2AV_MX8 && width % kMxGroup != 0) return false;
+    a->cap = c->capacity_rows;
+    a->in_row = a2av_row_bytes(i, c->k);
+    a->w_row = w == A2AV_MX4 ? c->k / 2 : w == A2AV_MX8 ? c->k : a2av_row_bytes(w, c->k);
+    a->out_row = a2av_row_bytes(o, width);
+    a->R = c->num_ranks;
+    a->epr = c->experts_per_rank;
+    a->G = a->R * a->epr;
+    a->K = c->k;
+    a->N = c->n;
+    a->width = width;
+    a->in_dtype = i;
+    a->w_dtype = w;
+    a->out_dtype = o;
+    a->swiglu = c->activation == A2AV_ACT_SWIGLU;
+    return true;
+}
+
+size_t alignment_of(int32_t dtype) { return dtype == A2AV_F32 ? 4 : dtype == A2AV_BF16 ? 2 : 16; }
+
+hipError_t launch_general(const ExpertArgs& a, int num_cu, hipStream_t st) {
+    const int64_t mt = std::min<int64_t>((a.R * a.cap + kGenM - 1) / kGenM + a.G, INT32_MAX);
+    const int cols = a.swiglu ? kGenN / 2 : kGenN;
+    const int64_t tiles = mt * ((a.width + cols - 1) / cols);
+    const unsigned grid = (unsigned)std::min<int64_t>(tiles, (int64_t)num_cu * 4);
+    hipLaunchKernelGGL(expert_general_kernel, dim3(grid), dim3(kGenThreads), 0, st, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace a2av
+
+extern "C" int a2av_expert_matmul(const a2av_matmul_t* cfg, const void* in, const int32_t* expert_offsets,
+                                  const void* weight, const void* weight_scales, void* out, uint32_t* status,
+                                  void* stream) {
+    using namespace a2av;
+    ExpertArgs a{};
+    if (!make_args(cfg, &a) || !expert_offsets || !status) return A2AV_ERR_INVALID;
+    if ((uintptr_t)status % 4 != 0 || (uintptr_t)expert_offsets % 4 != 0) return A2AV_ERR_INVALID;
+    const bool mx = a.w_dtype == A2AV_MX8 || a.w_dtype == A2AV_MX4;
+    if (!weight || mx != (weight_scales != nullptr)) return A2AV_ERR_INVALID;
+    if (a.cap > 0 && (!in || !out)) return A2AV_ERR_INVALID;
+    if ((uintptr_t)in % alignment_of(a.in_dtype) || (uintptr_t)weight % alignment_of(a.w_dtype) ||
+        (uintptr_t)out % alignment_of(a.out_dtype))
+        return A2AV_ERR_INVALID;
+    // out apart from everything that is read
+    const uintptr_t o = (uintptr_t)out, oe = o + (uintptr_t)(a.R * a.cap * a.out_row);
+    auto meets = [&](const void* p, int64_t n) { return p && (uintptr_t)p < oe && o < (uintptr_t)p + (uintptr_t)n; };
+    const int64_t wr = (int64_t)a.G * a.N;
+    if (meets(in, a.R * a.cap * a.in_row) || meets(weight, wr * a.w_row) ||
+        meets(weight_scales, wr * (a.K / kMxGroup)) || meets(expert_offsets, 4ll * a.R * (a.epr + 1)) || meets(status, 4))
+        return A2AV_ERR_INVALID;
+    if (a.cap == 0) return A2AV_OK;
+    int dev = 0, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+        return A2AV_ERR_HIP;
+    a.in = (const uint8_t*)in;
+    a.off = expert_offsets;
+    a.weight = (const uint8_t*)weight;
+    a.scales = (const uint8_t*)weight_scales;
+    a.out = (uint8_t*)out;
+    a.status = status;
+    return launch_general(a, cus, static_cast<hipStream_t>(stream)) == hipSuccess ? A2AV_OK : A2AV_ERR_HIP;
+}
