@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "liba2av.so")
 DEBUG_LIB = os.path.join(HERE, "liba2av_debug.so")
-SOURCES = ["a2av_api.hip", "a2av_kernels.hip", "a2av_measure.hip", "a2av_norm.hip", "a2av_experts.hip"]
+SOURCES = ["a2av_api.hip", "a2av_kernels.hip", "a2av_measure.hip", "a2av_norm.hip", "a2av_experts.hip",
+           "a2av_experts_tile.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

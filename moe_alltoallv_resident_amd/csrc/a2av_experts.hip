@@ -5,109 +5,13 @@
 // No host knows how many rows an expert got, so no grid can be cut to them: every block
 // reads the group starts, counts the row tiles of every expert into LDS and walks the tile
 // list (tile t, t + blocks, ...) until it ends.
-#include "../../include/a2av.h"
-#include "a2av_internal.h"
-#include "a2av_mx.h"
-
-#include <algorithm>
-#include <type_traits>
+// Here: the entry point and the general kernel.
+#include "a2av_experts.h"
 
 namespace a2av {
 namespace {
 
-constexpr int kWave = 64;
 constexpr int32_t kMaxDim = 1 << 20;
-constexpr uint32_t kStOffsets = 8u;
-static_assert(kStOffsets == A2AV_ST_OFFSETS, "status bit");
-
-struct ExpertArgs {
-    const uint8_t* in;
-    const int32_t* off;      // [R][epr + 1]
-    const uint8_t* weight;
-    const uint8_t* scales;
-    uint8_t* out;
-    uint32_t* status;
-    int64_t cap;
-    int64_t in_row;          // bytes of a row of in, weight and out
-    int64_t w_row;
-    int64_t out_row;
-    int32_t R, epr, G;       // G = R * epr groups
-    int32_t K, N;
-    int32_t width;           // columns that come out
-    int32_t in_dtype, w_dtype, out_dtype;
-    int32_t swiglu;
-};
-
-struct Group {
-    int64_t row;             // first row, counted over all slices
-    int32_t rows;
-};
-
-// Group g's rows: starts past the capacity are cut to it (a receive overflow), a start out
-// of order leaves the group empty.
-__device__ inline Group group_of(const ExpertArgs& a, int g, bool* bad) {
-    const int d = g / a.epr, le = g - d * a.epr;
-    const int32_t* p = a.off + (int64_t)d * (a.epr + 1) + le;
-    int32_t b = p[0], e = p[1];
-    if (b < 0 || e < b) {
-        *bad = true;
-        b = e = 0;
-    }
-    const int32_t cap = (int32_t)a.cap;
-    b = min(b, cap);
-    e = min(e, cap);
-    return Group{(int64_t)d * a.cap + b, e - b};
-}
-
-// Row tiles of every group, as ends[g] = tiles of groups 0 .. g; returns how many there are.
-// Every thread of the block calls it; `tiles(rows)` says how many tiles a group has.
-template <int THREADS, typename F>
-__device__ int count_tiles(const ExpertArgs& a, int* ends, int* wave_sum, F&& tiles) {
-    const int per = (a.G + THREADS - 1) / THREADS;
-    const int g0 = threadIdx.x * per;
-    int sum = 0;
-    bool bad = false;
-    for (int i = 0; i < per; ++i) {
-        if (g0 + i >= a.G) break;
-        sum += tiles(group_of(a, g0 + i, &bad).rows);
-        ends[g0 + i] = sum;
-    }
-    if (bad && blockIdx.x == 0) atomicOr(a.status, kStOffsets);
-    int scan = sum;
-#pragma unroll
-    for (int m = 1; m < kWave; m <<= 1) {
-        const int up = __shfl_up(scan, m);
-        if ((int)(threadIdx.x % kWave) >= m) scan += up;
-    }
-    if (threadIdx.x % kWave == kWave - 1) wave_sum[threadIdx.x / kWave] = scan;
-    __syncthreads();
-    int before = scan - sum, total = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / kWave; ++w) {
-        const int v = wave_sum[w];
-        if (w < (int)threadIdx.x / kWave) before += v;
-        total += v;
-    }
-    for (int i = 0; i < per; ++i) {
-        if (g0 + i >= a.G) break;
-        ends[g0 + i] += before;
-    }
-    __syncthreads();
-    return total;
-}
-
-// The group of row tile t: the first whose end is past t.
-__device__ inline int find_group(const int* ends, int G, int t) {
-    int lo = 0, hi = G - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (ends[mid] > t) hi = mid;
-        else lo = mid + 1;
-    }
-    return lo;
-}
-
-__device__ inline float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
 
 // ---- the general form ----------------------------------------------------------------
 // Any width, stride and alignment that the call allows: elements are read one by one,
@@ -249,7 +153,9 @@ bool make_args(const a2av_matmul_t* c, ExpertArgs* a) {
 
 size_t alignment_of(int32_t dtype) { return dtype == A2AV_F32 ? 4 : dtype == A2AV_BF16 ? 2 : 16; }
 
-hipError_t launch_general(const ExpertArgs& a, int num_cu, hipStream_t st) {
+}  // namespace
+
+hipError_t launch_experts_general(const ExpertArgs& a, int num_cu, hipStream_t st) {
     const int64_t mt = std::min<int64_t>((a.R * a.cap + kGenM - 1) / kGenM + a.G, INT32_MAX);
     const int cols = a.swiglu ? kGenN / 2 : kGenN;
     const int64_t tiles = mt * ((a.width + cols - 1) / cols);
@@ -258,7 +164,6 @@ hipError_t launch_general(const ExpertArgs& a, int num_cu, hipStream_t st) {
     return hipGetLastError();
 }
 
-}  // namespace
 }  // namespace a2av
 
 extern "C" int a2av_expert_matmul(const a2av_matmul_t* cfg, const void* in, const int32_t* expert_offsets,
@@ -292,5 +197,7 @@ extern "C" int a2av_expert_matmul(const a2av_matmul_t* cfg, const void* in, cons
     a.scales = (const uint8_t*)weight_scales;
     a.out = (uint8_t*)out;
     a.status = status;
-    return launch_general(a, cus, static_cast<hipStream_t>(stream)) == hipSuccess ? A2AV_OK : A2AV_ERR_HIP;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const hipError_t e = experts_tile_takes(a) ? launch_experts_tile(a, cus, st) : launch_experts_general(a, cus, st);
+    return e == hipSuccess ? A2AV_OK : A2AV_ERR_HIP;
 }

@@ -5,7 +5,15 @@ Bounds.  eps32 = 2^-24 is half a step of float32.  A float32 sum of n products i
 most n * 2 * eps32 * sum |products| (one rounding an addition and one a product, whatever
 the order; twice that where the matrix units may cut instead of round).  A rounding to the
 output type adds half a step: 2^-8 of the value for bfloat16, 2^-24 for float32, 2^-4 for
-e4m3 (or half of e4m3's smallest step, 2^-10 of the scale)."""
+e4m3 (or half of e4m3's smallest step, 2^-10 of the scale).
+
+8-bit rows meet their weights in the matrix unit's 8-bit form, which adds eight neighbouring
+products (elements 8i .. 8i + 7) at a time with the bits down to 2^-13 of the largest one's
+power of two and cuts what is below; the sums of eight are then added in float32.  (Seen on
+the GPU, products of powers of two: 2^16 - 2^16 + 2^(16-j) in one such eight is 2^(16-j) up to
+j = 13 and 0 from j = 14 on; with the third product in another eight it is 2^(16-j) at every j
+that e4m3 reaches, 24 and more.)  So each of the other seven products loses less than 2^-13 of
+the largest: at most 7 * 2^-13 * max|x| * max|w| for every eight, summed over the row."""
 import numpy as np
 import torch
 
@@ -106,12 +114,14 @@ def assert_mx8_close(rows, want, err, what):
     assert (rows[..., n + n // 32:row].cpu() == 0).all(), f"{what}: padding"
 
 
-def product(x, w, swiglu):
-    """Rows times weight rows in float64 with the bound of the float32 arithmetic:
-    returns (result, error before the output's rounding)."""
+def product(x, w, swiglu, eights=False):
+    """Rows times weight rows in float64 with the bound of the arithmetic (eights: 8-bit rows, see
+    above): returns (result, error before the output's rounding)."""
     k = x.shape[-1]
     v, m = x @ w.t(), x.abs() @ w.abs().t()
     err = 2 * (k + 2) * EPS32 * m
+    if eights:
+        err = err + 7 * 2.0 ** -13 * (x.abs().unflatten(-1, (-1, 8)).amax(-1) @ w.abs().unflatten(-1, (-1, 8)).amax(-1).t())
     if not swiglu:
         return v, err
     h = v.shape[-1] // 2

@@ -85,7 +85,7 @@ class Case:
                 untouched[d, a:b] = False
                 x = values(self.x[d, a:b], i, self.k)
                 wt = values(self.w[e], w, self.k, None if self.ws is None else self.ws[e])
-                want, err = product(x, wt, self.swiglu)
+                want, err = product(x, wt, self.swiglu, i == MX8)
                 what = f"rank {d} expert {le} rows {a}:{b}"
                 # after a bad start two groups may share rows: those hold either's, so nothing is said of them
                 one = owners[d, a:b] == 1
@@ -360,9 +360,9 @@ def test_the_layer_captured_and_replayed(weight):
                 if a == b:
                     continue
                 e = d * epr + le
-                h, err = product(values(s.recv[d, a:b], MX8, H), values(w1[e], weight, H, s1[e]), True)
+                h, err = product(values(s.recv[d, a:b], MX8, H), values(w1[e], weight, H, s1[e]), True, True)
                 assert_mx8_close(mid[d, a:b].cpu(), h, err, f"up {d} {le}")
-                o, err = product(values(mid[d, a:b], MX8, F), values(w2[e], weight, F, s2[e]), False)
+                o, err = product(values(mid[d, a:b], MX8, F), values(w2[e], weight, F, s2[e]), False, True)
                 assert_close(out[d, a:b].cpu().double(), o, err + (o.abs() + err) * HALF_STEP[BF16], f"down {d} {le}")
                 # this expert's rows stand in the order (source, token, slot)
                 at = (ids.cpu().flatten() == e).nonzero().flatten()
