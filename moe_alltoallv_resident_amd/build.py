@@ -16,7 +16,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "liba2av.so")
 DEBUG_LIB = os.path.join(HERE, "liba2av_debug.so")
 SOURCES = ["a2av_api.hip", "a2av_kernels.hip", "a2av_measure.hip", "a2av_norm.hip", "a2av_experts.hip",
-           "a2av_experts_tile.hip"]
+           "a2av_experts_few.hip", "a2av_experts_tile.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

@@ -104,10 +104,117 @@ __device__ inline int find_group(const int* ends, int G, int t) {
 
 __device__ inline float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
 
+// ---- what the matrix-unit kernels share ----------------------------------------------
+
+enum Kind { kF32, kBf16, kBf16Mx4, kMx8, kMx8Mx4 };      // rows and weights
+
+inline Kind kind_of(const ExpertArgs& a) {
+    if (a.in_dtype == A2AV_F32) return kF32;
+    if (a.in_dtype == A2AV_BF16) return a.w_dtype == A2AV_MX4 ? kBf16Mx4 : kBf16;
+    return a.w_dtype == A2AV_MX4 ? kMx8Mx4 : kMx8;
+}
+
+__host__ __device__ constexpr bool weight_scaled(int kind) { return kind >= kBf16Mx4; }
+__host__ __device__ constexpr bool rows_scaled(int kind) { return kind >= kMx8; }
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+[[maybe_unused]] constexpr uint32_t kOutside = 0x80000000u;   // an offset that every buffer check refuses: reads zero
+
+#ifdef A2AV_DEVICE_CODE
+__device__ inline __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00020000);
+}
+
+// 16 bytes a lane, from each lane's offset straight to 1024 neighbouring bytes of LDS.  Written as
+// an instruction without outputs: with the builtin the compiler waits for every such load before
+// the next read of any LDS, so that nothing could be loaded while a step is multiplied.  Whoever
+// reads the bytes calls wait_for_loads first, and a barrier where other wavefronts loaded them.
+__device__ inline void load_to_lds(u32x4 buf, const void* lds, uint32_t voffset, uint32_t soffset) {
+    const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(voffset), "s"(buf), "s"(__builtin_amdgcn_readfirstlane(soffset))
+                 : "memory");
+}
+
+// The same with 4 bytes a lane and 256 of LDS.
+__device__ inline void load_word_to_lds(u32x4 buf, const void* lds, uint32_t voffset, uint32_t soffset) {
+    const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(voffset), "s"(buf), "s"(__builtin_amdgcn_readfirstlane(soffset))
+                 : "memory");
+}
+
+// Waits until at most N of this wavefront's loads are on their way (they arrive in order).
+template <int N>
+__device__ inline void wait_for_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+// The buffer of `bytes` bytes at p as the four words that the instruction takes.
+__device__ inline u32x4 buffer_words(const uint8_t* p, uint32_t bytes) {
+    const uint64_t at = (uint64_t)(uintptr_t)p;
+    u32x4 w;
+    w[0] = __builtin_amdgcn_readfirstlane((uint32_t)at);
+    w[1] = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)) & 0xFFFFu;
+    w[2] = __builtin_amdgcn_readfirstlane(bytes);
+    w[3] = 0x00020000u;
+    return w;
+}
+
+// Eight E2M1 elements and the bits of their scale's power of two as eight bfloat16, exactly.
+__device__ inline u32x4 widen_e2m1(uint32_t q, float scale) {
+    u32x4 v;
+    v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 0));
+    v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 1));
+    v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 2));
+    v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 3));
+    return v;
+}
+
+// acc += w . x^T for 16 weight rows and 16 input rows: lane (l16, g) gives 16 bytes of weight row
+// l16 and of input row l16, the same elements of both, and holds columns 4g .. 4g + 3 of row l16.
+template <int KIND>
+__device__ inline f32x4 multiply16(u32x4 w, u32x4 x, f32x4 acc) {
+    if constexpr (KIND == kF32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[e]), __uint_as_float(x[e]), acc, 0, 0, 0);
+        return acc;
+    } else {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
+    }
+}
+
+// The same for 128 elements in 8 (rows) and 8 or 4 bits (weights) with their scale bytes.  8-bit
+// operands: lane group g gives elements 16g .. 16g + 15 (lo) and 64 + 16g .. 64 + 16g + 15 (hi) of
+// its row; 4-bit ones: 32g .. 32g + 31 (lo); the scale byte of elements 32g .. 32g + 31 is lane
+// group g's in both.
+template <int KIND>
+__device__ inline f32x4 multiply_scaled(u32x4 wlo, u32x4 whi, int ws, u32x4 xlo, u32x4 xhi, int xs, f32x4 acc) {
+    const i32x8 w = {(int)wlo[0], (int)wlo[1], (int)wlo[2], (int)wlo[3], (int)whi[0], (int)whi[1], (int)whi[2], (int)whi[3]};
+    const i32x8 x = {(int)xlo[0], (int)xlo[1], (int)xlo[2], (int)xlo[3], (int)xhi[0], (int)xhi[1], (int)xhi[2], (int)xhi[3]};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, KIND == kMx8 ? 0 : 4, 0, 0, ws, 0, xs);
+}
+#endif
+
+constexpr int kFewRows = 16;    // groups of at most so many rows are the few-rows kernel's
+
+// Whether the matrix-unit kernels take the call: rows and weights in whole 16-byte pieces, an
+// expert's weight and a tile's rows within 32-bit offsets.
+inline bool experts_mfma_takes(const ExpertArgs& a) {
+    return a.in_row % 16 == 0 && a.w_row % 16 == 0 && (uintptr_t)a.in % 16 == 0 && (uintptr_t)a.weight % 16 == 0 &&
+           a.N * a.w_row <= INT32_MAX && 256 * a.in_row <= INT32_MAX;
+}
+
 // The general kernel, for whatever the others do not take.
 hipError_t launch_experts_general(const ExpertArgs& a, int num_cu, hipStream_t st);
-// The matrix-unit tiles.
-bool experts_tile_takes(const ExpertArgs& a);
+// Groups of 1 .. kFewRows rows.
+hipError_t launch_experts_few(const ExpertArgs& a, int num_cu, hipStream_t st);
+// Groups of more rows.
 hipError_t launch_experts_tile(const ExpertArgs& a, int num_cu, hipStream_t st);
 
 }  // namespace a2av

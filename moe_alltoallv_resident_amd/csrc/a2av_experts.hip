@@ -198,6 +198,13 @@ extern "C" int a2av_expert_matmul(const a2av_matmul_t* cfg, const void* in, cons
     a.out = (uint8_t*)out;
     a.status = status;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const hipError_t e = experts_tile_takes(a) ? launch_experts_tile(a, cus, st) : launch_experts_general(a, cus, st);
+    hipError_t e;
+    if (experts_mfma_takes(a)) {
+        // a group of more rows needs a capacity of more
+        e = launch_experts_few(a, cus, st);
+        if (e == hipSuccess && a.cap > kFewRows) e = launch_experts_tile(a, cus, st);
+    } else {
+        e = launch_experts_general(a, cus, st);
+    }
     return e == hipSuccess ? A2AV_OK : A2AV_ERR_HIP;
 }

@@ -15,26 +15,17 @@
 namespace a2av {
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-enum Kind { kF32, kBf16, kBf16Mx4, kMx8, kMx8Mx4 };
-
 constexpr int kThreads = 512, kWaves = kThreads / kWave;
 constexpr int kTileN = 256;              // weight rows of a tile
 constexpr int kMaxM = 256;               // input rows of the largest tile
 constexpr int kRowStep = 128;            // bytes of an input row in a step
 constexpr int kSuper = 8;                // row tiles that are walked together
-[[maybe_unused]] constexpr uint32_t kOutside = 0x80000000u;   // an offset that every buffer check refuses: reads zero
 
 __host__ __device__ constexpr int weight_step(int kind) {        // bytes of a weight row in a step
     return kind == kBf16Mx4 ? 32 : kind == kMx8Mx4 ? 64 : 128;
 }
 [[maybe_unused]] __host__ __device__ constexpr int step_elems(int kind) {   // elements of a step
     return kind == kF32 ? 32 : kind == kBf16 || kind == kBf16Mx4 ? 64 : 128; }
-__host__ __device__ constexpr bool weight_scaled(int kind) { return kind >= kBf16Mx4; }
-__host__ __device__ constexpr bool rows_scaled(int kind) { return kind >= kMx8; }
 
 template <int KIND>
 struct Stage {
@@ -61,27 +52,6 @@ __device__ inline int piece_at(int r, int p) {
     else return p;
 }
 
-#ifdef A2AV_DEVICE_CODE
-__device__ inline __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* p, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00020000);
-}
-
-// 16 bytes a lane, from each lane's offset to 1024 neighbouring bytes of LDS.
-__device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t buf, uint8_t* lds, uint32_t voffset, uint32_t soffset) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (__attribute__((address_space(3))) void*)lds, 16, (int)voffset, (int)soffset,
-                                             0, 0);
-}
-#endif
-
-// Up to four scale bytes from `at` on, of which the first `n` are the row's.
-[[maybe_unused]] __device__ inline uint32_t load_scales(const uint8_t* at, int n, bool whole) {
-    if (whole) return *(const uint32_t*)at;
-    uint32_t v = 0;
-    for (int i = 0; i < 4; ++i)
-        if (i < n) v |= (uint32_t)at[i] << (8 * i);
-    return v;
-}
-
 // Everything of a tile that does not depend on its height.
 struct Tile {
     const uint8_t* in;       // its first row
@@ -104,8 +74,8 @@ __device__ __forceinline__ void run_tile(const ExpertArgs& a, const Tile& t, Sta
     const int x_bytes = KIND == kF32 ? a.K * 4 : KIND == kBf16 || KIND == kBf16Mx4 ? a.K * 2 : a.K;
     const int x_tail = x_bytes - (steps - 1) * kRowStep, w_tail = (int)a.w_row - (steps - 1) * kWStep;
 
-    const __amdgpu_buffer_rsrc_t xbuf = buffer_of(t.in, (uint32_t)(t.rows * a.in_row));
-    const __amdgpu_buffer_rsrc_t wbuf = buffer_of(t.weight, (uint32_t)(a.N * a.w_row));
+    const u32x4 xbuf = buffer_words(t.in, (uint32_t)(t.rows * a.in_row));
+    const u32x4 wbuf = buffer_words(t.weight, (uint32_t)(a.N * a.w_row));
     // Byte offsets of this lane's pieces; rows past the tile's, columns past the last one and, in
     // the last step, pieces past the row's end read zeros.
     uint32_t xo[kXLoads], wo[kWLoads];
@@ -129,40 +99,45 @@ __device__ __forceinline__ void run_tile(const ExpertArgs& a, const Tile& t, Sta
         wo[i] = wr < 0 ? kOutside : (uint32_t)(wr * a.w_row + c * 16);
         wt[i] = c * 16 < w_tail;
     }
-    auto load = [&](int s) {
-        Stage<KIND>& st = stage[s & 1];
+    auto load = [&](int s, Stage<KIND>* st) __attribute__((always_inline)) {
         const bool last = s == steps - 1;
 #pragma unroll
         for (int i = 0; i < kXLoads; ++i)
             if (32 * MT / 8 % kWaves == 0 || i * kWaves + wave < 32 * MT / 8)
-                load_to_lds(xbuf, st.x + (i * kWaves + wave) * 1024, last && !xt[i] ? kOutside : xo[i], s * kRowStep);
+                load_to_lds(xbuf, st->x + (i * kWaves + wave) * 1024, last && !xt[i] ? kOutside : xo[i], s * kRowStep);
 #pragma unroll
         for (int i = 0; i < kWLoads; ++i)
-            load_to_lds(wbuf, st.w + (i * kWaves + wave) * 1024, last && !wt[i] ? kOutside : wo[i], s * kWStep);
+            load_to_lds(wbuf, st->w + (i * kWaves + wave) * 1024, last && !wt[i] ? kOutside : wo[i], s * kWStep);
     };
-    // Scale bytes go through a register: thread i holds weight row i's, thread 256 + i input row i's.
-    constexpr int kSteps = step_elems(KIND) / kMxGroup;     // scale bytes of a step
+    // Scale bytes, a 32-bit word of four a row: wavefronts 0 .. 3 load the weight's, 4 .. 7 the input
+    // rows'.  Rows of scales that are not whole words (a width that is no multiple of 128) are
+    // read byte by byte instead, without a step's head start.
     const int blocks = a.K / kMxGroup;
-    const uint8_t* sp = nullptr;
-    bool whole = false;
+    const bool whole = blocks % 4 == 0 && (uintptr_t)t.scales % 4 == 0;
+    const u32x4 sbuf = buffer_words(wave < 4 ? t.scales : t.in,
+                                    wave < 4 ? (uint32_t)a.N * (uint32_t)blocks : (uint32_t)(t.rows * a.in_row));
+    uint32_t so = kOutside;
     if constexpr (weight_scaled(KIND)) {
-        if (threadIdx.x < kTileN) {
+        if (wave < 4) {
             const int wr = weight_row(threadIdx.x);
-            if (wr >= 0) sp = t.scales + (int64_t)wr * blocks;
-            whole = kSteps == 4 && blocks % 4 == 0 && (uintptr_t)t.scales % 4 == 0;
-        } else if (rows_scaled(KIND)) {
-            const int r = threadIdx.x - kTileN;
-            if (r < t.rows) sp = t.in + (int64_t)r * a.in_row + a.K;
-            whole = blocks % 4 == 0;
+            if (wr >= 0) so = (uint32_t)(wr * blocks);
+        } else if (rows_scaled(KIND) && (int)threadIdx.x - kTileN < t.rows) {
+            so = (uint32_t)((threadIdx.x - kTileN) * a.in_row + a.K);
         }
     }
-    auto scales_of = [&](int s) -> uint32_t {
-        return sp ? load_scales(sp + s * kSteps, min(kSteps, blocks - s * kSteps), whole) : 0u;
-    };
-    auto put_scales = [&](int s, uint32_t v) {
-        Stage<KIND>& st = stage[s & 1];
-        if (threadIdx.x < kTileN) st.ws[threadIdx.x] = v;
-        else if (rows_scaled(KIND)) st.xs[threadIdx.x - kTileN] = v;
+    auto load_scales = [&](int s, Stage<KIND>* st) __attribute__((always_inline)) {
+        if (!rows_scaled(KIND) && wave >= 4) return;
+        uint32_t* to = wave < 4 ? st->ws : st->xs;
+        const int first = s * step_elems(KIND) / kMxGroup / 4 * 4;      // the word's first block
+        if (whole) {
+            load_word_to_lds(sbuf, to + wave % 4 * kWave, so, first);
+        } else {
+            const uint8_t* p = wave < 4 ? t.scales : t.in;
+            uint32_t v = 0;
+            for (int i = 0; i < 4; ++i)
+                if (so != kOutside && first + i < blocks) v |= (uint32_t)p[so + first + i] << (8 * i);
+            to[wave % 4 * kWave + lane] = v;
+        }
     };
 
     f32x4 acc[MT][4];
@@ -171,17 +146,13 @@ __device__ __forceinline__ void run_tile(const ExpertArgs& a, const Tile& t, Sta
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-    __syncthreads();                                        // the tile before has been read
-    load(0);
-    if constexpr (weight_scaled(KIND)) put_scales(0, scales_of(0));
-    for (int s = 0; s < steps; ++s) {
-        __syncthreads();                                    // step s is in LDS, step s - 1 has been read
-        uint32_t next = 0;
+    // One step: the next one's loads begin, then this one's pieces are multiplied.
+    auto step = [&](int s, Stage<KIND>* into, const Stage<KIND>* from) __attribute__((always_inline)) {
+        const Stage<KIND>& st = *from;
         if (s + 1 < steps) {
-            load(s + 1);
-            if constexpr (weight_scaled(KIND)) next = scales_of(s + 1);
+            load(s + 1, into);
+            if constexpr (weight_scaled(KIND)) load_scales(s + 1, into);
         }
-        const Stage<KIND>& st = stage[s & 1];
         if constexpr (KIND == kF32 || KIND == kBf16 || KIND == kBf16Mx4) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -191,11 +162,7 @@ __device__ __forceinline__ void run_tile(const ExpertArgs& a, const Tile& t, Sta
                     const int r = wn * 64 + j * 16 + l16;
                     if constexpr (KIND == kBf16Mx4) {
                         const uint32_t q = *(const uint32_t*)(st.w + r * kWStep + k * 16 + g * 4);
-                        const float f = __uint_as_float((st.ws[r] >> (8 * k) & 255u) << 23);
-                        w[j][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, f, 0));
-                        w[j][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, f, 1));
-                        w[j][2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, f, 2));
-                        w[j][3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, f, 3));
+                        w[j] = widen_e2m1(q, __uint_as_float((uint32_t)((const uint8_t*)&st.ws[r])[s % 2 * 2 + k] << 23));
                     } else {
                         w[j] = *(const u32x4*)(st.w + place<128>(r, k * 4 + g));
                     }
@@ -205,51 +172,36 @@ __device__ __forceinline__ void run_tile(const ExpertArgs& a, const Tile& t, Sta
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if constexpr (KIND == kF32) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[j][e]), __uint_as_float(x[i][e]),
-                                                                                 acc[i][j], 0, 0, 0);
-                        } else {
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[j]),
-                                                                                __builtin_bit_cast(bf16x8, x[i]), acc[i][j], 0, 0, 0);
-                        }
-                    }
+                    for (int j = 0; j < 4; ++j) acc[i][j] = multiply16<KIND>(w[j], x[i], acc[i][j]);
             }
         } else {
-            // The 8-bit operand of 128 elements: lane group g holds elements 16g .. 16g + 15 and
-            // 64 + 16g .. 64 + 16g + 15 of its row; the 4-bit one 32g .. 32g + 31; the scale byte of
-            // elements 32g .. 32g + 31 is lane group g's in both.
-            i32x8 w[4];
+            u32x4 lo[4], hi[4];
             int sw[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int r = wn * 64 + j * 16 + l16;
-                u32x4 lo, hi = {0, 0, 0, 0};
-                if constexpr (KIND == kMx8) {
-                    lo = *(const u32x4*)(st.w + place<128>(r, g));
-                    hi = *(const u32x4*)(st.w + place<128>(r, 4 + g));
-                } else {
-                    lo = *(const u32x4*)(st.w + place<64>(r, g));
-                }
-                w[j] = i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+                lo[j] = *(const u32x4*)(st.w + place<kWStep>(r, g));
+                if constexpr (KIND == kMx8) hi[j] = *(const u32x4*)(st.w + place<kWStep>(r, 4 + g));
+                else hi[j] = u32x4{0, 0, 0, 0};
                 sw[j] = ((const uint8_t*)&st.ws[r])[g];
             }
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 const int r = (wm * MT + i) * 16 + l16;
-                const u32x4 lo = *(const u32x4*)(st.x + place<128>(r, g)), hi = *(const u32x4*)(st.x + place<128>(r, 4 + g));
-                const i32x8 x = {(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+                const u32x4 xlo = *(const u32x4*)(st.x + place<128>(r, g)), xhi = *(const u32x4*)(st.x + place<128>(r, 4 + g));
                 const int sx = ((const uint8_t*)&st.xs[r])[g];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[j], x, acc[i][j], KIND == kMx8 ? 0 : 4, 0, 0,
-                                                                                 sw[j], 0, sx);
+                for (int j = 0; j < 4; ++j) acc[i][j] = multiply_scaled<KIND>(lo[j], hi[j], sw[j], xlo, xhi, sx, acc[i][j]);
             }
         }
-        if constexpr (weight_scaled(KIND))
-            if (s + 1 < steps) put_scales(s + 1, next);
+    };
+    __syncthreads();                                        // the tile before has been read
+    load(0, &stage[0]);
+    if constexpr (weight_scaled(KIND)) load_scales(0, &stage[0]);
+    for (int s = 0; s < steps; ++s) {
+        wait_for_loads<0>();
+        __syncthreads();                                    // step s is in LDS, step s - 1 has been read
+        step(s, &stage[(s + 1) & 1], &stage[s & 1]);
     }
 
     // Results: lane (l16, g) has columns 4g .. 4g + 3 of a 16 x 16 piece, of input row l16.
@@ -329,7 +281,7 @@ __global__ void __launch_bounds__(kThreads) expert_tile_kernel(ExpertArgs a) {
     __shared__ Stage<KIND> stage[2];
     __shared__ int ends[kMaxExperts];
     __shared__ int wave_sum[kWaves];
-    const int mt = count_tiles<kThreads>(a, ends, wave_sum, [](int rows) { return (rows + kMaxM - 1) / kMaxM; });
+    const int mt = count_tiles<kThreads>(a, ends, wave_sum, [](int rows) { return rows > kFewRows ? (rows + kMaxM - 1) / kMaxM : 0; });
     const int cols = a.swiglu ? kTileN / 2 : kTileN;
     const int nt = (a.width + cols - 1) / cols;
     const int64_t total = (int64_t)mt * nt;
@@ -364,19 +316,7 @@ hipError_t launch(const ExpertArgs& a, int num_cu, hipStream_t st) {
     return hipGetLastError();
 }
 
-Kind kind_of(const ExpertArgs& a) {
-    if (a.in_dtype == A2AV_F32) return kF32;
-    if (a.in_dtype == A2AV_BF16) return a.w_dtype == A2AV_MX4 ? kBf16Mx4 : kBf16;
-    return a.w_dtype == A2AV_MX4 ? kMx8Mx4 : kMx8;
-}
-
 }  // namespace
-
-// Rows and weights in whole 16-byte pieces, an expert's weight within a 32-bit offset.
-bool experts_tile_takes(const ExpertArgs& a) {
-    return a.in_row % 16 == 0 && a.w_row % 16 == 0 && (uintptr_t)a.in % 16 == 0 && (uintptr_t)a.weight % 16 == 0 &&
-           a.N * a.w_row <= INT32_MAX && kMaxM * a.in_row <= INT32_MAX;
-}
 
 hipError_t launch_experts_tile(const ExpertArgs& a, int num_cu, hipStream_t st) {
     switch (kind_of(a)) {
