@@ -292,7 +292,8 @@ int a2av_rmsnorm(const void* x, const void* residual, const void* weight, void* 
 typedef struct {
     int32_t num_ranks;          /* R >= 1 */
     int32_t experts_per_rank;   /* R * experts_per_rank <= 4096 */
-    int64_t capacity_rows;      /* rows of each rank's slice of in and out, 0 .. 2^31 - 1 */
+    int64_t capacity_rows;      /* rows of each rank's slice of in and out; R * capacity_rows
+                                   < 2^31 */
     int32_t k;                  /* elements of an input row, 1 .. 2^20 */
     int32_t n;                  /* rows of an expert's weight, 1 .. 2^20 */
     int32_t in_dtype;           /* A2AV_F32, A2AV_BF16 or A2AV_MX8 */

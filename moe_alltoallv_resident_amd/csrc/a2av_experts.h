@@ -12,6 +12,7 @@
 namespace a2av {
 
 constexpr int kWave = 64;
+constexpr int kTileRows = 256;           // input rows and weight rows of a tile of the matrix-unit kernel
 constexpr uint32_t kStOffsets = 8u;
 static_assert(kStOffsets == A2AV_ST_OFFSETS, "status bit");
 
@@ -31,6 +32,8 @@ struct ExpertArgs {
     int32_t width;           // columns that come out
     int32_t in_dtype, w_dtype, out_dtype;
     int32_t swiglu;
+    int32_t few;             // groups of at most so many rows are the few-rows kernel's
+    int32_t tile_least;      // fewer tiles than this of larger groups are too
 };
 
 struct Group {
@@ -54,17 +57,56 @@ __device__ inline Group group_of(const ExpertArgs& a, int g, bool* bad) {
     return Group{(int64_t)d * a.cap + b, e - b};
 }
 
-// Row tiles of every group, as ends[g] = tiles of groups 0 .. g; returns how many there are.
-// Every thread of the block calls it; `tiles(rows)` says how many tiles a group has.
+__host__ __device__ inline int pieces_of(int rows, int each) { return rows / each + (rows % each != 0); }
+
+// Sums of four counts over all groups, `counts(rows)` each; every thread of the block calls it and
+// has them afterwards.
+struct Four {
+    int v[4];
+};
 template <int THREADS, typename F>
-__device__ int count_tiles(const ExpertArgs& a, int* ends, int* wave_sum, F&& tiles) {
-    const int per = (a.G + THREADS - 1) / THREADS;
+__device__ Four count_groups(const ExpertArgs& a, int* wave_sum, F&& counts) {
+    Four sum = {{0, 0, 0, 0}};
+    bool bad = false;
+    for (int g = threadIdx.x; g < a.G; g += THREADS) {
+        const Four c = counts(group_of(a, g, &bad).rows);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum.v[k] += c.v[k];
+    }
+    if (bad && blockIdx.x == 0) atomicOr(a.status, kStOffsets);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int m = 1; m < kWave; m <<= 1) sum.v[k] += __shfl_xor(sum.v[k], m);
+        if (threadIdx.x % kWave == 0) wave_sum[threadIdx.x / kWave * 4 + k] = sum.v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        int v = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / kWave; ++w) v += wave_sum[w * 4 + k];
+        sum.v[k] = v;
+    }
+    __syncthreads();
+    return sum;
+}
+
+// Row tiles of every `each` groups, as ends[i] = tiles of groups 0 .. each * (i + 1) - 1; returns how
+// many there are.  Every thread of the block calls it; `tiles(rows)` says how many tiles a group has.
+template <int THREADS, typename F>
+__device__ int count_tiles(const ExpertArgs& a, int* ends, int* wave_sum, F&& tiles, int each = 1) {
+    const int n = (a.G + each - 1) / each;
+    const int per = (n + THREADS - 1) / THREADS;
     const int g0 = threadIdx.x * per;
     int sum = 0;
     bool bad = false;
     for (int i = 0; i < per; ++i) {
-        if (g0 + i >= a.G) break;
-        sum += tiles(group_of(a, g0 + i, &bad).rows);
+        if (g0 + i >= n) break;
+        for (int k = 0; k < each; ++k) {
+            const int g = (g0 + i) * each + k;
+            if (g < a.G) sum += tiles(group_of(a, g, &bad).rows);
+        }
         ends[g0 + i] = sum;
     }
     if (bad && blockIdx.x == 0) atomicOr(a.status, kStOffsets);
@@ -84,11 +126,17 @@ __device__ int count_tiles(const ExpertArgs& a, int* ends, int* wave_sum, F&& ti
         total += v;
     }
     for (int i = 0; i < per; ++i) {
-        if (g0 + i >= a.G) break;
+        if (g0 + i >= n) break;
         ends[g0 + i] += before;
     }
     __syncthreads();
     return total;
+}
+
+// Tiles of the groups of more than a.few rows, over the output's width.
+__device__ inline int64_t large_tiles(const ExpertArgs& a, int row_tiles) {
+    const int cols = a.swiglu ? kTileRows / 2 : kTileRows;
+    return (int64_t)row_tiles * ((a.width + cols - 1) / cols);
 }
 
 // The group of row tile t: the first whose end is past t.
@@ -133,18 +181,12 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* p, uint32_t by
 // reads the bytes calls wait_for_loads first, and a barrier where other wavefronts loaded them.
 __device__ inline void load_to_lds(u32x4 buf, const void* lds, uint32_t voffset, uint32_t soffset) {
     const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds;
+    u32x4 b;                                             // scalar registers, whatever the compiler thinks of it
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = __builtin_amdgcn_readfirstlane(buf[i]);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
-                 : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(voffset), "s"(buf), "s"(__builtin_amdgcn_readfirstlane(soffset))
-                 : "memory");
-}
-
-// The same with 4 bytes a lane and 256 of LDS.
-__device__ inline void load_word_to_lds(u32x4 buf, const void* lds, uint32_t voffset, uint32_t soffset) {
-    const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                 :
-                 : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(voffset), "s"(buf), "s"(__builtin_amdgcn_readfirstlane(soffset))
+                 : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(voffset), "s"(b), "s"(__builtin_amdgcn_readfirstlane(soffset))
                  : "memory");
 }
 
@@ -152,6 +194,21 @@ __device__ inline void load_word_to_lds(u32x4 buf, const void* lds, uint32_t vof
 template <int N>
 __device__ inline void wait_for_loads() {
     asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+// A barrier that waits for this wavefront's LDS reads and writes alone, not for its loads and stores.
+__device__ inline void block_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" : : : "memory");
+}
+
+// Lanes of this wavefront hand each other values through LDS: what was written before it is read
+// after it (LDS instructions of a wavefront are carried out in order).
+__device__ inline void wave_sync() {
+    asm volatile("" : : : "memory");
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("" : : : "memory");
 }
 
 // The buffer of `bytes` bytes at p as the four words that the instruction takes.
@@ -201,8 +258,6 @@ __device__ inline f32x4 multiply_scaled(u32x4 wlo, u32x4 whi, int ws, u32x4 xlo,
 }
 #endif
 
-constexpr int kFewRows = 16;    // groups of at most so many rows are the few-rows kernel's
-
 // Whether the matrix-unit kernels take the call: rows and weights in whole 16-byte pieces, an
 // expert's weight and a tile's rows within 32-bit offsets.
 inline bool experts_mfma_takes(const ExpertArgs& a) {
@@ -212,7 +267,10 @@ inline bool experts_mfma_takes(const ExpertArgs& a) {
 
 // The general kernel, for whatever the others do not take.
 hipError_t launch_experts_general(const ExpertArgs& a, int num_cu, hipStream_t st);
-// Groups of 1 .. kFewRows rows.
+// Groups of 1 .. a.few rows; of more as well, in pieces of a.few, where they would make tiles for
+// fewer than half of the CUs (a.tile_least).
+int few_rows(const ExpertArgs& a);
+bool few_rows_all(const ExpertArgs& a);
 hipError_t launch_experts_few(const ExpertArgs& a, int num_cu, hipStream_t st);
 // Groups of more rows.
 hipError_t launch_experts_tile(const ExpertArgs& a, int num_cu, hipStream_t st);

@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kGenThreads) expert_general_kernel(ExpertArgs 
     __shared__ float xs[kGenM][kGenK + 1];
     __shared__ float ws[kGenN][kGenK + 1];
     __shared__ float res[kGenM][kGenN + 1];
-    const int mt = count_tiles<kGenThreads>(a, ends, wave_sum, [](int rows) { return (rows + kGenM - 1) / kGenM; });
+    const int mt = count_tiles<kGenThreads>(a, ends, wave_sum, [](int rows) { return pieces_of(rows, kGenM); });
     const int cols = a.swiglu ? kGenN / 2 : kGenN;       // output columns of a tile
     const int nt = (a.width + cols - 1) / cols;
     const int tm = threadIdx.x / 16 * 2, tn = threadIdx.x % 16 * 4;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kGenThreads) expert_general_kernel(ExpertArgs 
 bool make_args(const a2av_matmul_t* c, ExpertArgs* a) {
     if (!c || c->num_ranks < 1 || c->experts_per_rank < 1) return false;
     if ((int64_t)c->num_ranks * c->experts_per_rank > kMaxExperts) return false;
-    if (c->capacity_rows < 0 || c->capacity_rows > INT32_MAX) return false;
+    if (c->capacity_rows < 0 || c->capacity_rows > INT32_MAX / c->num_ranks) return false;   // rows are int32
     if (c->k < 1 || c->k > kMaxDim || c->n < 1 || c->n > kMaxDim) return false;
     const int32_t i = c->in_dtype, w = c->weight_dtype, o = c->out_dtype;
     const bool types = (i == A2AV_F32 && w == A2AV_F32 && o == A2AV_F32) ||
@@ -200,9 +200,14 @@ extern "C" int a2av_expert_matmul(const a2av_matmul_t* cfg, const void* in, cons
     hipStream_t st = static_cast<hipStream_t>(stream);
     hipError_t e;
     if (experts_mfma_takes(a)) {
-        // a group of more rows needs a capacity of more
+        a.few = few_rows(a);
+        a.tile_least = few_rows_all(a) ? cus / 2 : 0;
         e = launch_experts_few(a, cus, st);
-        if (e == hipSuccess && a.cap > kFewRows) e = launch_experts_tile(a, cus, st);
+        // a group of more rows needs a capacity of more, and a tile's worth of groups needs rows enough
+        // (a group of r > few rows makes at most r / few row tiles)
+        const int64_t most = a.cap > a.few ? a.R * a.cap / a.few : 0;
+        const int cols = a.swiglu ? kTileRows / 2 : kTileRows;
+        if (e == hipSuccess && most * ((a.width + cols - 1) / cols) >= std::max(a.tile_least, 1)) e = launch_experts_tile(a, cus, st);
     } else {
         e = launch_experts_general(a, cus, st);
     }

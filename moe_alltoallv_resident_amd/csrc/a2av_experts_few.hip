@@ -1,17 +1,25 @@
-// The experts' products for experts with at most 16 rows: a decode step's case, bound by
-// reading the weights, each of which meets 16 rows at most.
+// The experts' products for experts with few rows: a decode step's case, bound by reading the
+// weights.
 //
-// A wavefront takes 16 or 32 weight rows and a part of their length, loads them straight into
-// registers in the matrix instruction's layout (nothing is shared, so nothing goes through
-// LDS) and multiplies them with all the rows at once; rows that are not there read zeros and
-// cost no memory.  The parts of a weight row's length are added through LDS.
+// Many tiles (a whole batch's step): a block streams 128 weight rows through LDS, 128 bytes of
+// each at a time in a ring of two to four stages that are loaded straight from memory, and
+// multiplies them with up to 64 input rows.  Whole 128-byte pieces matter: read into registers in
+// the matrix instruction's layout, 64 bytes of sixteen rows at a time, the weights came at 4.3
+// TB/s only.
+//
+// Few tiles (one token): a wavefront takes 16 weight rows and a part of their length straight into
+// registers, so that as many CUs as possible read; the parts are added through LDS.
 #include "a2av_experts.h"
 
 namespace a2av {
 namespace {
 
-constexpr int kThreads = 512, kWaves = kThreads / kWave;
+[[maybe_unused]] constexpr int kThreads = 512, kWaves = kThreads / kWave;
 constexpr int kBlocksPerCu = 2;
+constexpr int kDirectRows = 16;          // rows that the direct form takes at most
+[[maybe_unused]] constexpr int kStreamRows = 128;     // weight rows of a stream tile
+[[maybe_unused]] constexpr int kStreamLds = 79872;    // of a block: half of a CU's but for the list of groups
+[[maybe_unused]] constexpr int kCoarse = 8;               // beyond 512 groups `ends` has an entry for so many
 
 // Elements of a unit, the step of the walk along a row: 16 bytes of a weight row for each lane
 // (32 with 8-bit weights).
@@ -27,11 +35,11 @@ __device__ inline u32x4 load16(__amdgpu_buffer_rsrc_t buf, uint32_t off) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(buf, (int)off, 0, 0));
 }
 
-template <int KIND, int NT>
+template <int KIND>
 struct Batch {
-    u32x4 w[batch_units(KIND)][NT][w_pieces(KIND)];
+    u32x4 w[batch_units(KIND)][w_pieces(KIND)];
     u32x4 x[batch_units(KIND)][x_pieces(KIND)];
-    uint8_t ws[batch_units(KIND)][NT], xs[batch_units(KIND)];
+    uint8_t ws[batch_units(KIND)], xs[batch_units(KIND)];
 };
 #endif
 
@@ -40,15 +48,58 @@ struct Job {
     const uint8_t* weight;   // its expert's
     const uint8_t* scales;
     uint8_t* out;
-    int rows;                // 1 .. 16
+    int rows;                // 1 .. few
     int col0;                // the tile's first output column
 };
 
-// NT: 16-row pieces of a wavefront.  A tile is kWaves / parts times 16 * NT weight rows.
-// With SwiGLU the two pieces are 16 columns' gate and up rows, one piece 8 columns' both.
-template <int KIND, int NT>
-__device__ __forceinline__ void run_job(const ExpertArgs& a, const Job& t, int parts, f32x4* part) {
 #ifdef A2AV_DEVICE_CODE
+// Writes four neighbouring columns of a row, in float32, as the output type.  With 8-bit rows the
+// eight lanes of a scale's 32 columns call it together.
+template <int KIND>
+__device__ __forceinline__ void write_four(const ExpertArgs& a, uint8_t* row, int c, f32x4 v, bool on) {
+    on = on && c < a.width;
+    if (rows_scaled(KIND) && a.out_dtype == A2AV_MX8) {
+        uint32_t mx = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx = max(mx, abs_bits(v[e]));
+#pragma unroll
+        for (int s = 1; s < 8; s <<= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, s));
+        const uint32_t sb = mx_scale_byte(mx);
+        const float f = mx_inverse(sb);
+        if (on) {
+            *(uint32_t*)(row + c) = mx8_pack(v[0] * f, v[1] * f, v[2] * f, v[3] * f, sb == 255u);
+            if (c % kMxGroup == 0) row[a.width + c / kMxGroup] = (uint8_t)sb;
+            if (c + 4 == a.width)
+                for (int b = a.width + a.width / kMxGroup; b < a.out_row; ++b) row[b] = 0;
+        }
+    } else if (on) {
+        if constexpr (KIND == kF32) {
+            float* p = (float*)row + c;
+            if (a.width % 4 == 0 && (uintptr_t)a.out % 16 == 0) *(f32x4*)p = v;
+            else
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < a.width) p[e] = v[e];
+        } else {
+            u16* p = (u16*)row + c;
+            uint32_t b[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[e] = f32_to_bf16(v[e]);
+            if (a.width % 4 == 0 && (uintptr_t)a.out % 8 == 0) *(u32x2*)p = u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16};
+            else
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < a.width) p[e] = (u16)b[e];
+        }
+    }
+}
+
+// ---- few tiles: straight into registers ----------------------------------------------
+
+// A tile is kWaves / parts times 16 weight rows.  With SwiGLU a wavefront's 16 are 8 columns'
+// gate rows and their up rows.
+template <int KIND>
+__device__ __forceinline__ void run_direct(const ExpertArgs& a, const Job& t, int parts, f32x4* part) {
     constexpr int kUnit = unit_elems(KIND), kBatch = batch_units(KIND);
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane % 16, g = lane / 16;
@@ -60,34 +111,19 @@ __device__ __forceinline__ void run_job(const ExpertArgs& a, const Job& t, int p
     const __amdgpu_buffer_rsrc_t wbuf = buffer_of(t.weight, (uint32_t)(a.N * a.w_row));
     __amdgpu_buffer_rsrc_t sbuf = wbuf;
     if constexpr (weight_scaled(KIND)) sbuf = buffer_of(t.scales, (uint32_t)a.N * (uint32_t)blocks);
-    int wr[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        int c, up = 0;
-        if (!a.swiglu) {
-            c = t.col0 + (wrow * NT + j) * 16 + l16;
-        } else if (NT == 2) {
-            c = t.col0 + wrow * 16 + l16;
-            up = j;
-        } else {
-            c = t.col0 + wrow * 8 + l16 % 8;
-            up = l16 / 8;
-        }
-        wr[j] = c < a.width ? c + up * a.width : -1;
-    }
+    const int c = a.swiglu ? t.col0 + wrow * 8 + l16 % 8 : t.col0 + wrow * 16 + l16;
+    const int wr = c < a.width ? (a.swiglu ? c + l16 / 8 * a.width : c) : -1;
     // Lane (l16, g)'s elements of unit u, as byte offsets; outside a row they read zeros.
-    auto load = [&](Batch<KIND, NT>& b, int at) {
+    auto load = [&](Batch<KIND>& b, int at) __attribute__((always_inline)) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int unit = at + u;
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int p = 0; p < w_pieces(KIND); ++p) {
-                    const uint32_t o = (KIND == kMx8 ? unit * 128 + p * 64 : unit * 64) + g * 16;
-                    const bool on = unit < units && o < (uint32_t)a.w_row && wr[j] >= 0;
-                    b.w[u][j][p] = load16(wbuf, on ? (uint32_t)(wr[j] * a.w_row) + o : kOutside);
-                }
+            for (int p = 0; p < w_pieces(KIND); ++p) {
+                const uint32_t o = (KIND == kMx8 ? unit * 128 + p * 64 : unit * 64) + g * 16;
+                const bool on = unit < units && o < (uint32_t)a.w_row && wr >= 0;
+                b.w[u][p] = load16(wbuf, on ? (uint32_t)(wr * a.w_row) + o : kOutside);
+            }
 #pragma unroll
             for (int p = 0; p < x_pieces(KIND); ++p) {
                 uint32_t o, end;
@@ -101,46 +137,39 @@ __device__ __forceinline__ void run_job(const ExpertArgs& a, const Job& t, int p
                     o = unit * 64 + g * 16;
                     end = (uint32_t)a.in_row;
                 }
-                const bool on = unit < units && o < end;        // rows past the last are past the buffer's end
+                const bool on = unit < units && o < end;     // rows past the last are past the buffer's end
                 b.x[u][p] = load16(xbuf, on ? (uint32_t)(l16 * a.in_row) + o : kOutside);
             }
             if constexpr (weight_scaled(KIND)) {
                 const int blk = unit * 4 + g;
                 const bool on = unit < units && blk < blocks;
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    b.ws[u][j] = __builtin_amdgcn_raw_buffer_load_b8(sbuf, on && wr[j] >= 0 ? (int)((uint32_t)(wr[j] * blocks) + blk) : (int)kOutside,
-                                                                     0, 0);
+                b.ws[u] = __builtin_amdgcn_raw_buffer_load_b8(sbuf, on && wr >= 0 ? (int)((uint32_t)(wr * blocks) + blk) : (int)kOutside, 0, 0);
                 if constexpr (rows_scaled(KIND))
                     b.xs[u] = __builtin_amdgcn_raw_buffer_load_b8(xbuf, on ? (int)(l16 * a.in_row + a.K + blk) : (int)kOutside, 0, 0);
             }
         }
     };
-    f32x4 acc[NT];
+    f32x4 acc = {0, 0, 0, 0};
+    auto use = [&](const Batch<KIND>& b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j] = f32x4{0, 0, 0, 0};
-    auto use = [&](const Batch<KIND, NT>& b) {
+        for (int u = 0; u < kBatch; ++u) {
+            if constexpr (KIND == kF32 || KIND == kBf16) {
+                acc = multiply16<KIND>(b.w[u][0], b.x[u][0], acc);
+            } else if constexpr (KIND == kBf16Mx4) {
+                const float f = __uint_as_float((uint32_t)b.ws[u] << 23);
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                if constexpr (KIND == kF32 || KIND == kBf16) {
-                    acc[j] = multiply16<KIND>(b.w[u][j][0], b.x[u][0], acc[j]);
-                } else if constexpr (KIND == kBf16Mx4) {
-                    const float f = __uint_as_float((uint32_t)b.ws[u][j] << 23);
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) acc[j] = multiply16<KIND>(widen_e2m1(b.w[u][j][0][p], f), b.x[u][p], acc[j]);
-                } else {
-                    const u32x4 none = {0, 0, 0, 0};
-                    acc[j] = multiply_scaled<KIND>(b.w[u][j][0], KIND == kMx8 ? b.w[u][j][w_pieces(KIND) - 1] : none, b.ws[u][j],
-                                                   b.x[u][0], b.x[u][x_pieces(KIND) - 1], b.xs[u], acc[j]);
-                }
+                for (int p = 0; p < 4; ++p) acc = multiply16<KIND>(widen_e2m1(b.w[u][0][p], f), b.x[u][p], acc);
+            } else {
+                const u32x4 none = {0, 0, 0, 0};
+                acc = multiply_scaled<KIND>(b.w[u][0], KIND == kMx8 ? b.w[u][w_pieces(KIND) - 1] : none, b.ws[u], b.x[u][0],
+                                            b.x[u][x_pieces(KIND) - 1], b.xs[u], acc);
             }
+        }
     };
     // The parts take batches in turn, so that together they sweep along their rows.
     {
         const int step = parts * kBatch;
-        Batch<KIND, NT> b0, b1;
+        Batch<KIND> b0, b1;
         load(b0, wpart * kBatch);
         for (int at = wpart * kBatch; at < units; at += 2 * step) {
             load(b1, at + step);
@@ -150,104 +179,261 @@ __device__ __forceinline__ void run_job(const ExpertArgs& a, const Job& t, int p
         }
     }
 
-    // part[wave][j][lane]: the parts of a row are neighbours
-#pragma unroll
-    for (int j = 0; j < NT; ++j) part[(wave * NT + j) * kWave + lane] = acc[j];
+    part[wave * kWave + lane] = acc;                         // the parts of a row are neighbours
     __syncthreads();
-    const int groups = kWaves / parts;
-    const int cols = groups * 16 * NT / (a.swiglu ? 2 : 1);
+    const int cols = kWaves / parts * 16 / (a.swiglu ? 2 : 1);
     const int quads = cols / 4;                              // four neighbouring columns: one lane's result
-    auto sum = [&](int row, int j, int ln) {
-        f32x4 v = part[(row * parts * NT + j) * kWave + ln];
-        for (int p = 1; p < parts; ++p) v += part[((row * parts + p) * NT + j) * kWave + ln];
+    auto sum = [&](int row, int ln) {
+        f32x4 v = part[row * parts * kWave + ln];
+        for (int p = 1; p < parts; ++p) v += part[(row * parts + p) * kWave + ln];
         return v;
     };
     for (int i = threadIdx.x; i < 16 * quads; i += kThreads) {
         const int m = i / quads, q = i % quads;
         f32x4 v;
         if (!a.swiglu) {
-            v = sum(q / 4 / NT, q / 4 % NT, m + 16 * (q % 4));
+            v = sum(q / 4, m + 16 * (q % 4));
         } else {
-            f32x4 up;
-            if (NT == 2) {
-                v = sum(q / 4, 0, m + 16 * (q % 4));
-                up = sum(q / 4, NT - 1, m + 16 * (q % 4));
-            } else {
-                v = sum(q / 2, 0, m + 16 * (q % 2));
-                up = sum(q / 2, 0, m + 16 * (q % 2 + 2));
-            }
+            v = sum(q / 2, m + 16 * (q % 2));
+            const f32x4 up = sum(q / 2, m + 16 * (q % 2 + 2));
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = silu_mul(v[e], up[e]);
         }
-        const int c = t.col0 + 4 * q;
-        const bool on = m < t.rows && c < a.width;
-        uint8_t* out = t.out + m * a.out_row;
-        if (rows_scaled(KIND) && a.out_dtype == A2AV_MX8) {
-            // a scale's 32 columns are eight neighbouring threads' (the tile has a multiple of 32)
-            uint32_t mx = 0;
+        write_four<KIND>(a, t.out + m * a.out_row, t.col0 + 4 * q, v, m < t.rows);
+    }
+    __syncthreads();                                         // `part` is free again
+}
+
+// ---- many tiles: a stream through LDS ------------------------------------------------
+
+// A stage: 128 bytes of each of 128 weight rows, and the same elements of 16 * MT input rows.
+template <int KIND, int MT>
+struct Ring {
+    static constexpr int kElems = KIND == kF32 ? 32 : KIND == kBf16 ? 64 : KIND == kMx8 ? 128 : 256;
+    static constexpr int kXRow = KIND == kMx8Mx4 ? 256 : KIND == kBf16Mx4 ? 512 : 128;   // bytes of an input row
+    static constexpr int kXBytes = 16 * MT * kXRow;
+    static constexpr int kStage = kStreamRows * 128 + kXBytes;
+    static constexpr int kScales = weight_scaled(KIND) ? 2 * (kStreamRows + 64) * 16 : 0;   // bytes behind the stages
+    // as many stages as fit half of a CU's LDS, four at most
+    static constexpr int kFit = (kStreamLds - kScales) / kStage;
+    static constexpr int kDepth = kFit > 4 ? 4 : kFit > 3 && weight_scaled(KIND) ? 3 : kFit;
+    static_assert(kDepth >= 2, "two stages at least");
+    static constexpr int kXLoads = kXBytes / 1024;           // of all wavefronts for a stage
+    static constexpr int kXPer = (kXLoads + kWaves - 1) / kWaves;
+    static constexpr int kResult = 16 * MT * (kStreamRows + 4) * 4;
+    static_assert(kResult <= kDepth * kStage, "results fit the ring");
+};
+
+// Place of 16-byte piece c of row r in LDS rows of ROW bytes: eight rows' same pieces, read by
+// eight neighbouring lanes, fall into different banks.
+template <int ROW>
+__device__ inline int place_of(int r, int c) {
+    return r * ROW + ((c ^ (r & 7)) << 4);
+}
+
+template <int KIND, int MT>
+__device__ __forceinline__ void run_stream(const ExpertArgs& a, const Job& t, uint8_t* lds) {
+    using R = Ring<KIND, MT>;
+    constexpr int kXRow = R::kXRow, kXPieces = kXRow / 16, kDepth = R::kDepth;
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int l16 = lane % 16, g = lane / 16;
+    const int steps = (a.K + R::kElems - 1) / R::kElems;
+    const int x_bytes = KIND == kF32 ? a.K * 4 : KIND == kBf16 || KIND == kBf16Mx4 ? a.K * 2 : a.K;
+    const int blocks = a.K / kMxGroup;
+    uint8_t* scales = lds + kDepth * R::kStage;              // two times sixteen blocks' bytes of the weight and input rows
+
+    const u32x4 xbuf = buffer_words(t.in, (uint32_t)(t.rows * a.in_row));
+    const u32x4 wbuf = buffer_words(t.weight, (uint32_t)(a.N * a.w_row));
+    // wavefront w's 16 rows of the tile; with SwiGLU 8 columns' gate rows and their up rows
+    auto weight_row = [&](int r) {
+        const int c = a.swiglu ? t.col0 + r / 16 * 8 + r % 8 : t.col0 + r;
+        return c < a.width ? (a.swiglu ? c + r / 8 % 2 * a.width : c) : -1;
+    };
+    uint32_t wo[2], xo[R::kXPer];
+    const int wc = ((lane % 8) ^ (lane / 8)) * 16;           // load i: tile rows 16 * wave + 8 i ..
+    const bool w_over = wc >= (int)a.w_row - (steps - 1) * 128;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx = max(mx, abs_bits(v[e]));
+    for (int i = 0; i < 2; ++i) {
+        const int wr = weight_row(wave * 16 + i * 8 + lane / 8);
+        wo[i] = wr < 0 ? kOutside : (uint32_t)(wr * a.w_row + wc);
+    }
+    bool x_over[R::kXPer];
 #pragma unroll
-            for (int s = 1; s < 8; s <<= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, s));
-            const uint32_t sb = mx_scale_byte(mx);
-            const float f = mx_inverse(sb);
-            if (on) {
-                *(uint32_t*)(out + c) = mx8_pack(v[0] * f, v[1] * f, v[2] * f, v[3] * f, sb == 255u);
-                if (c % kMxGroup == 0) out[a.width + c / kMxGroup] = (uint8_t)sb;
-                if (c + 4 == a.width)
-                    for (int b = a.width + a.width / kMxGroup; b < a.out_row; ++b) out[b] = 0;
+    for (int i = 0; i < R::kXPer; ++i) {
+        const int r = (i * kWaves + wave) * (1024 / kXRow) + lane / kXPieces, c = ((lane % kXPieces) ^ (r & 7)) * 16;
+        xo[i] = (uint32_t)(r * a.in_row + c);                // rows past the last: past the buffer's end
+        x_over[i] = c >= x_bytes - (steps - 1) * kXRow;
+    }
+    // Wavefronts 0 and 1 load the weight rows' scale bytes, 2 the input rows', sixteen blocks at once.
+    const bool scale_wave = weight_scaled(KIND) && wave < (rows_scaled(KIND) ? 3 : 2);
+    const u32x4 sbuf = buffer_words(wave < 2 ? t.scales : t.in, wave < 2 ? (uint32_t)a.N * (uint32_t)blocks : (uint32_t)(t.rows * a.in_row));
+    uint32_t so = kOutside;
+    if (weight_scaled(KIND) && wave < 2) {
+        const int wr = weight_row(wave * 64 + lane);
+        if (wr >= 0) so = (uint32_t)(wr * blocks);
+    } else if (rows_scaled(KIND) && wave == 2 && lane < t.rows) {
+        so = (uint32_t)(lane * a.in_row + a.K);
+    }
+    constexpr int kBlocks = R::kElems / kMxGroup;            // of a stage
+    const bool x_wave = R::kXLoads % kWaves == 0 || (R::kXPer - 1) * kWaves + wave < R::kXLoads;   // makes all kXPer loads
+    // Past the last stage everything reads zeros: the counts that the waits go by stay the same.
+    auto load = [&](int s) __attribute__((always_inline)) {
+        uint8_t* st = lds + s % kDepth * R::kStage;
+        if (weight_scaled(KIND) && scale_wave && s * kBlocks % 16 == 0 && s < steps)
+            load_to_lds(sbuf, scales + (s * kBlocks / 16 % 2) * ((kStreamRows + 64) * 16) + wave * 1024, so, s * kBlocks);
+        const bool in = s < steps, last = s == steps - 1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            load_to_lds(wbuf, st + wave * 2048 + i * 1024, in && !(last && w_over) ? wo[i] : kOutside, s * 128);
+#pragma unroll
+        for (int i = 0; i < R::kXPer; ++i)
+            if (i + 1 < R::kXPer || x_wave)
+                load_to_lds(xbuf, st + kStreamRows * 128 + (i * kWaves + wave) * 1024, in && !(last && x_over[i]) ? xo[i] : kOutside,
+                            s * kXRow);
+    };
+    f32x4 acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < kDepth - 1; ++s) load(s);
+    for (int s = 0; s < steps; ++s) {
+        // stage s has landed when only the later stages' loads are on their way
+        if (x_wave) wait_for_loads<(kDepth - 2) * (2 + R::kXPer)>();
+        else wait_for_loads<(kDepth - 2) * (1 + R::kXPer)>();
+        block_barrier();                                     // for everyone, and stage s - 1 has been read
+        load(s + kDepth - 1);
+        const uint8_t* wst = lds + s % kDepth * R::kStage + wave * 2048;
+        const uint8_t* xst = lds + s % kDepth * R::kStage + kStreamRows * 128;
+        const uint8_t* sc = scales + (s * kBlocks / 16 % 2) * ((kStreamRows + 64) * 16) + s * kBlocks % 16;
+        const u32x4 w0 = *(const u32x4*)(wst + place_of<128>(l16, g)), w1 = *(const u32x4*)(wst + place_of<128>(l16, 4 + g));
+        if constexpr (KIND == kF32 || KIND == kBf16) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const int r = i * 16 + l16;
+                acc[i] = multiply16<KIND>(w0, *(const u32x4*)(xst + place_of<kXRow>(r, g)), acc[i]);
+                acc[i] = multiply16<KIND>(w1, *(const u32x4*)(xst + place_of<kXRow>(r, 4 + g)), acc[i]);
             }
-        } else if (on) {
-            if constexpr (KIND == kF32) {
-                float* p = (float*)out + c;
-                if (a.width % 4 == 0 && (uintptr_t)a.out % 16 == 0) *(f32x4*)p = v;
-                else
-                    for (int e = 0; e < 4; ++e)
-                        if (c + e < a.width) p[e] = v[e];
-            } else {
-                u16* p = (u16*)out + c;
-                uint32_t b[4];
+        } else if constexpr (KIND == kBf16Mx4) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) b[e] = f32_to_bf16(v[e]);
-                if (a.width % 4 == 0 && (uintptr_t)a.out % 8 == 0) *(u32x2*)p = u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16};
-                else
-                    for (int e = 0; e < 4; ++e)
-                        if (c + e < a.width) p[e] = (u16)b[e];
+            for (int u = 0; u < 2; ++u) {
+                if (u && s * kBlocks + 4 >= blocks) break;   // the row ends after 128 elements: no scales here
+                // a lane's 16 bytes are 32 elements, a scale's
+                const float f = __uint_as_float((uint32_t)sc[(wave * 16 + l16) * 16 + u * 4 + g] << 23);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const u32x4 w = widen_e2m1(u ? w1[p] : w0[p], f);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        acc[i] = multiply16<KIND>(w, *(const u32x4*)(xst + place_of<kXRow>(i * 16 + l16, (u * 4 + g) * 4 + p)), acc[i]);
+                }
+            }
+        } else {
+            constexpr int kUnits = KIND == kMx8 ? 1 : 2;     // of 128 elements
+            const u32x4 none = {0, 0, 0, 0};
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                if (u && s * kBlocks + 4 >= blocks) break;
+                const int ws = sc[(wave * 16 + l16) * 16 + u * 4 + g];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const int r = i * 16 + l16;
+                    const int xs = sc[(kStreamRows + r) * 16 + u * 4 + g];
+                    acc[i] = multiply_scaled<KIND>(u ? w1 : w0, KIND == kMx8 ? w1 : none, ws,
+                                                   *(const u32x4*)(xst + place_of<kXRow>(r, u * 8 + g)),
+                                                   *(const u32x4*)(xst + place_of<kXRow>(r, u * 8 + 4 + g)), xs, acc[i]);
+                }
             }
         }
     }
-    __syncthreads();                                         // `part` is free again
-#endif
+    wait_for_loads<0>();
+    block_barrier();                                         // LDS is free
+    float* res = (float*)lds;                                // [16 * MT][kStreamRows + 4]
+    constexpr int kPitch = kStreamRows + 4;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) *(f32x4*)(res + (i * 16 + l16) * kPitch + wave * 16 + 4 * g) = acc[i];
+    __syncthreads();
+    const int quads = kStreamRows / (a.swiglu ? 8 : 4);
+    for (int i = threadIdx.x; i < 16 * MT * quads; i += kThreads) {
+        const int m = i / quads, q = i % quads;
+        const float* row = res + m * kPitch;
+        f32x4 v;
+        if (!a.swiglu) {
+            v = *(const f32x4*)(row + 4 * q);
+        } else {
+            v = *(const f32x4*)(row + q / 2 * 16 + q % 2 * 4);
+            const f32x4 up = *(const f32x4*)(row + q / 2 * 16 + 8 + q % 2 * 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = silu_mul(v[e], up[e]);
+        }
+        write_four<KIND>(a, t.out + m * a.out_row, t.col0 + 4 * q, v, m < t.rows);
+    }
+    block_barrier();                                         // LDS is free again
 }
+#endif
 
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 2 * kBlocksPerCu) expert_few_kernel(ExpertArgs a) {
-    __shared__ int ends[kMaxExperts];
-    __shared__ int wave_sum[kWaves];
-    __shared__ f32x4 part[kWaves * 2 * kWave];
-    const int n = count_tiles<kThreads>(a, ends, wave_sum, [](int rows) { return rows > 0 && rows <= kFewRows ? 1 : 0; });
-    if (n == 0) return;
-    const int64_t pieces = (int64_t)n * ((a.N + 15) / 16);   // of 16 weight rows
-    const int batches = (a.K + unit_elems(KIND) * batch_units(KIND) - 1) / (unit_elems(KIND) * batch_units(KIND));
-    const bool two = pieces >= 4 * (int64_t)gridDim.x;
-    const int wide = two ? 2 : 1;
-    const int most = a.out_dtype != A2AV_MX8 ? 8 : a.swiglu ? 2 * wide : 4 * wide;   // a tile of 8-bit rows has 32 columns at least
-    int parts = 1;
-    while (parts < most && parts < batches) parts *= 2;
-    const int cols = kWaves / parts * 16 * wide / (a.swiglu ? 2 : 1);
-    const int nt = (a.width + cols - 1) / cols;
-    const int64_t total = (int64_t)n * nt;
-    for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
-        const int i = __builtin_amdgcn_readfirstlane((int)(t / nt)), tn = __builtin_amdgcn_readfirstlane((int)(t % nt));
-        const int grp = __builtin_amdgcn_readfirstlane(find_group(ends, a.G, i));
+#ifdef A2AV_DEVICE_CODE
+    __shared__ __align__(1024) uint8_t lds[kStreamLds];
+    __shared__ int ends[kMaxExperts / kCoarse];
+    const int per = a.G > kMaxExperts / kCoarse ? kCoarse : 1;      // groups of an entry of `ends`
+    const int cols_stream = a.swiglu ? kStreamRows / 2 : kStreamRows;
+    const int nt_stream = (a.width + cols_stream - 1) / cols_stream;
+    const int chunk = a.few;                                 // rows of a stream tile
+    // The groups of more than `lo` and at most `hi` rows, in pieces of `chunk` rows.
+    int lo = 0, hi = a.few;
+    auto pieces = [&](int rows) { return rows > lo && rows <= hi ? pieces_of(rows, chunk) : 0; };
+    auto list = [&] { return __builtin_amdgcn_readfirstlane(count_tiles<kThreads>(a, ends, (int*)lds, pieces, per)); };
+    auto job_at = [&](int i, int col0) {
+        const int e = __builtin_amdgcn_readfirstlane(find_group(ends, (a.G + per - 1) / per, i));
+        int left = i - (e ? __builtin_amdgcn_readfirstlane(ends[e - 1]) : 0);
+        int grp = e * per;
         bool bad = false;
-        const Group gr = group_of(a, grp, &bad);
-        const int64_t w0 = (int64_t)grp * a.N;
-        const Job job{a.in + gr.row * a.in_row, a.weight + w0 * a.w_row, a.scales + w0 * (a.K / kMxGroup),
-                      a.out + gr.row * a.out_row, __builtin_amdgcn_readfirstlane(gr.rows), tn * cols};
-        if (two) run_job<KIND, 2>(a, job, parts, part);
-        else run_job<KIND, 1>(a, job, parts, part);
+        Group gr = group_of(a, grp, &bad);
+        // no round unless an entry has several groups
+        for (int p; grp + 1 < a.G && left >= (p = pieces(gr.rows)); gr = group_of(a, ++grp, &bad)) left -= p;
+        grp = __builtin_amdgcn_readfirstlane(grp);
+        const int64_t w0 = (int64_t)grp * a.N, row = gr.row + (int64_t)left * chunk;
+        return Job{a.in + row * a.in_row, a.weight + w0 * a.w_row, a.scales + w0 * (a.K / kMxGroup), a.out + row * a.out_row,
+                   __builtin_amdgcn_readfirstlane(min(chunk, gr.rows - left * chunk)), col0};
+    };
+    // stream tiles of the small groups and of all, row tiles of the large ones, groups for the direct form
+    const Four n4 = count_groups<kThreads>(a, (int*)lds, [&](int rows) {
+        return Four{{rows <= chunk && rows > 0, pieces_of(rows, chunk), rows > chunk ? pieces_of(rows, kTileRows) : 0,
+                     rows > 0 && rows <= kDirectRows}};
+    });
+    const bool all = large_tiles(a, n4.v[2]) < a.tile_least;
+    if (all) hi = INT32_MAX;
+    int n = __builtin_amdgcn_readfirstlane(all ? n4.v[1] : n4.v[0]);
+    if (n == 0) return;
+    const bool direct = __builtin_amdgcn_readfirstlane(n4.v[3]) > 0 &&
+                        (a.few == kDirectRows || (int64_t)n * nt_stream < gridDim.x / kBlocksPerCu);
+    if (direct) {
+        // Not a stream tile for every CU: groups of up to 16 rows go by smaller pieces.  Every row's
+        // length is cut into as many parts as a block has wavefronts.
+        const int limit = hi;
+        hi = kDirectRows;
+        n = list();
+        const int batches = (a.K + unit_elems(KIND) * batch_units(KIND) - 1) / (unit_elems(KIND) * batch_units(KIND));
+        const int most = a.out_dtype != A2AV_MX8 ? 8 : a.swiglu ? 2 : 4;   // a tile of 8-bit rows has 32 columns at least
+        int parts = 1;
+        while (parts < most && parts < batches) parts *= 2;
+        const int cols = kWaves / parts * 16 / (a.swiglu ? 2 : 1);
+        const int nt = (a.width + cols - 1) / cols;
+        for (int64_t t = blockIdx.x; t < (int64_t)n * nt; t += gridDim.x)
+            run_direct<KIND>(a, job_at((int)(t / nt), (int)(t % nt) * cols), parts, (f32x4*)lds);
+        if (a.few == kDirectRows) return;
+        lo = kDirectRows;
+        hi = limit;
     }
+    n = list();
+    for (int64_t t = blockIdx.x; t < (int64_t)n * nt_stream; t += gridDim.x) {
+        const Job job = job_at((int)(t / nt_stream), (int)(t % nt_stream) * cols_stream);
+        if (job.rows <= 16) run_stream<KIND, 1>(a, job, lds);
+        else if (KIND == kBf16Mx4 || job.rows <= 32) run_stream<KIND, 2>(a, job, lds);
+        else if constexpr (KIND != kBf16Mx4) run_stream<KIND, 4>(a, job, lds);
+    }
+#endif
 }
 
 template <int KIND>
@@ -257,6 +443,16 @@ hipError_t launch(const ExpertArgs& a, int num_cu, hipStream_t st) {
 }
 
 }  // namespace
+
+// The stream takes up to 64 input rows, 32 of bfloat16 with 4-bit weights (their 256 elements of a
+// stage are 512 bytes); its scales are loaded in whole words.
+int few_rows(const ExpertArgs& a) {
+    const Kind k = kind_of(a);
+    if (weight_scaled(k) && (a.K % 128 != 0 || (uintptr_t)a.scales % 4 != 0)) return kDirectRows;
+    return k == kBf16Mx4 ? 32 : 64;
+}
+
+bool few_rows_all(const ExpertArgs& a) { return a.few > kDirectRows; }
 
 hipError_t launch_experts_few(const ExpertArgs& a, int num_cu, hipStream_t st) {
     switch (kind_of(a)) {

@@ -116,6 +116,36 @@ def test_products(kind, swiglu, counts, k, n):
     Case(counts, k, n, kind, swiglu).run().check()
 
 
+# groups of every tile height and row tiles for more than half of the GPU's units
+BIG = [[300, 1100, 700, 20], [257, 129, 65, 600]]
+
+
+@kinds
+@pytest.mark.parametrize("swiglu", [False, True], ids=["plain", "swiglu"])
+@pytest.mark.parametrize("k,n", [(32, 2112), (96, 2112), (416, 2112), (128, 2560), (640, 2112)])
+def test_many_rows(kind, swiglu, k, n):
+    banner(f"many rows {kind} swiglu {swiglu} k {k} n {n}")
+    Case(BIG, k, n, kind, swiglu).run().check()
+
+
+def test_many_rows_repeat_bit_for_bit():
+    for kind in (KINDS[0], KINDS[1], KINDS[2], KINDS[4], KINDS[5]):
+        c = Case(BIG, 1024, 2112, kind, True).run()
+        torch.cuda.synchronize()
+        want = c.out.clone()
+        for _ in range(5):
+            c.out.fill_(77)
+            c.run()
+        torch.cuda.synchronize()
+        assert torch.equal(c.out, want)
+
+
+@pytest.mark.parametrize("kind", [KINDS[0], KINDS[1]], ids=["f32", "bf16"])
+def test_many_rows_of_odd_widths(kind):
+    for k, n, swiglu in ((104, 2090, False), (104, 2090, True), (200, 2051, False), (64, 2050, True)):
+        Case(BIG, k, n, kind, swiglu).run().check()
+
+
 @pytest.mark.parametrize("kind", [KINDS[0], KINDS[1]], ids=["f32", "bf16"])
 @pytest.mark.parametrize("k,n,offset", [(1, 2, 0), (7, 6, 0), (33, 34, 0), (130, 154, 0), (1001, 70, 0), (64, 66, 1),
                                         (256, 128, 3), (72, 10, 0), (200, 130, 0)])

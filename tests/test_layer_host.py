@@ -61,7 +61,7 @@ FPW = dict(weight_dtype=a2av.MX4, scales=P(5))
 
 @pytest.mark.parametrize("bad", [
     dict(num_ranks=0), dict(experts_per_rank=0), dict(num_ranks=64, experts_per_rank=65), dict(capacity_rows=-1),
-    dict(capacity_rows=1 << 31), dict(k=0), dict(n=0), dict(k=(1 << 20) + 1), dict(n=(1 << 20) + 1),
+    dict(capacity_rows=1 << 31), dict(capacity_rows=1 << 30), dict(k=0), dict(n=0), dict(k=(1 << 20) + 1), dict(n=(1 << 20) + 1),
     dict(in_dtype=a2av.F32), dict(in_dtype=a2av.MX4), dict(weight_dtype=a2av.F32), dict(weight_dtype=a2av.MX8, scales=P(5)),
     dict(out_dtype=a2av.F32), dict(out_dtype=a2av.MX8), dict(activation=2), dict(n=65, activation=a2av.ACT_SWIGLU),
     dict(MXW, k=48), dict(FPW, k=48), dict(MXW, n=48, out_dtype=a2av.MX8),
