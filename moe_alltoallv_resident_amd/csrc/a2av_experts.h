@@ -139,18 +139,43 @@ __device__ inline int64_t large_tiles(const ExpertArgs& a, int row_tiles) {
     return (int64_t)row_tiles * ((a.width + cols - 1) / cols);
 }
 
-// The group of row tile t: the first whose end is past t.
-__device__ inline int find_group(const int* ends, int G, int t) {
-    int lo = 0, hi = G - 1;
+// The list of row tiles has an entry for every group, or for every kCoarse of more than kEntries.
+constexpr int kCoarse = 8, kEntries = kMaxExperts / kCoarse;
+__device__ inline int groups_an_entry(const ExpertArgs& a) { return a.G > kEntries ? kCoarse : 1; }
+
+struct Piece {
+    int group;
+    Group rows;
+    int n;                   // which of the group's row tiles
+};
+
+// Row tile t of the list that count_tiles made with the same `tiles`.  All in scalar registers.
+template <typename F>
+__device__ inline Piece find_piece(const ExpertArgs& a, const int* ends, int each, int t, F&& tiles) {
+    int lo = 0, hi = (a.G + each - 1) / each - 1;            // the first entry whose end is past t
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (ends[mid] > t) hi = mid;
         else lo = mid + 1;
     }
-    return lo;
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    int left = t - (lo ? __builtin_amdgcn_readfirstlane(ends[lo - 1]) : 0), grp = lo * each;
+    bool bad = false;
+    Group gr = group_of(a, grp, &bad);
+    // no round unless an entry has several groups
+    for (int p; each > 1 && grp + 1 < a.G && left >= (p = tiles(gr.rows)); gr = group_of(a, ++grp, &bad)) left -= p;
+    return Piece{__builtin_amdgcn_readfirstlane(grp), gr, __builtin_amdgcn_readfirstlane(left)};
 }
 
-__device__ inline float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+// silu(g) * u.  The reciprocal is the hardware's (one step in the last place), an exact division
+// takes ten instructions for nothing that survives the output's rounding.
+__device__ inline float silu_mul(float g, float u) {
+#ifdef A2AV_DEVICE_CODE
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+#else
+    return 0.0f;
+#endif
+}
 
 // ---- what the matrix-unit kernels share ----------------------------------------------
 
@@ -175,6 +200,33 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* p, uint32_t by
     return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00020000);
 }
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// acc += w . x^T for 32 weight rows and 32 input rows: lane (l32, h) gives 32 bytes, w0 and w1, of
+// weight row l32 and the same elements of input row l32, and holds columns 8q + 4h .. 8q + 4h + 3 of
+// row l32 in acc[4q] .. acc[4q + 3].  64 bytes of each row: 16 float32, 32 bfloat16 or 64 8-bit
+// elements, of which w0 and x0 are the 16-byte piece h, w1 and x1 the piece 2 + h (4-bit weights: w0
+// alone, elements 32h .. 32h + 31); byte BYTE of ws and xs is the scale of elements 32h .. 32h + 31.
+template <int KIND, int BYTE>
+__device__ inline f32x16 multiply32(u32x4 w0, u32x4 w1, int ws, u32x4 x0, u32x4 x1, int xs, f32x16 acc) {
+    if constexpr (KIND == kF32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(w0[e]), __uint_as_float(x0[e]), acc, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(w1[e]), __uint_as_float(x1[e]), acc, 0, 0, 0);
+        return acc;
+    } else if constexpr (KIND == kBf16 || KIND == kBf16Mx4) {
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w0), __builtin_bit_cast(bf16x8, x0), acc, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w1), __builtin_bit_cast(bf16x8, x1), acc, 0, 0, 0);
+    } else {
+        const i32x8 w = {(int)w0[0], (int)w0[1], (int)w0[2], (int)w0[3], (int)w1[0], (int)w1[1], (int)w1[2], (int)w1[3]};
+        const i32x8 x = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc, KIND == kMx8 ? 0 : 4, 0, BYTE, ws, BYTE, xs);
+    }
+}
+
 // 16 bytes a lane, from each lane's offset straight to 1024 neighbouring bytes of LDS.  Written as
 // an instruction without outputs: with the builtin the compiler waits for every such load before
 // the next read of any LDS, so that nothing could be loaded while a step is multiplied.  Whoever
@@ -185,6 +237,18 @@ __device__ inline void load_to_lds(u32x4 buf, const void* lds, uint32_t voffset,
 #pragma unroll
     for (int i = 0; i < 4; ++i) b[i] = __builtin_amdgcn_readfirstlane(buf[i]);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(voffset), "s"(b), "s"(__builtin_amdgcn_readfirstlane(soffset))
+                 : "memory");
+}
+
+// The same with 4 bytes a lane and 256 of LDS.
+__device__ inline void load_word_to_lds(u32x4 buf, const void* lds, uint32_t voffset, uint32_t soffset) {
+    const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds;
+    u32x4 b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = __builtin_amdgcn_readfirstlane(buf[i]);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(voffset), "s"(b), "s"(__builtin_amdgcn_readfirstlane(soffset))
                  : "memory");

@@ -36,21 +36,23 @@ constexpr int kGenThreads = 256;
 constexpr int kGenM = 32, kGenN = 64, kGenK = 32;   // rows, weight rows and elements of a step
 
 __global__ void __launch_bounds__(kGenThreads) expert_general_kernel(ExpertArgs a) {
-    __shared__ int ends[kMaxExperts];
+    __shared__ int ends[kEntries];
     __shared__ int wave_sum[kGenThreads / kWave];
     __shared__ float xs[kGenM][kGenK + 1];
     __shared__ float ws[kGenN][kGenK + 1];
     __shared__ float res[kGenM][kGenN + 1];
-    const int mt = count_tiles<kGenThreads>(a, ends, wave_sum, [](int rows) { return pieces_of(rows, kGenM); });
+    auto pieces = [](int rows) { return pieces_of(rows, kGenM); };
+    const int each = groups_an_entry(a);
+    const int mt = count_tiles<kGenThreads>(a, ends, wave_sum, pieces, each);
     const int cols = a.swiglu ? kGenN / 2 : kGenN;       // output columns of a tile
     const int nt = (a.width + cols - 1) / cols;
     const int tm = threadIdx.x / 16 * 2, tn = threadIdx.x % 16 * 4;
     for (int64_t t = blockIdx.x; t < (int64_t)mt * nt; t += gridDim.x) {
-        const int t_m = (int)(t / nt), col0 = (int)(t % nt) * cols;
-        const int g = find_group(ends, a.G, t_m);
-        bool bad = false;
-        const Group grp = group_of(a, g, &bad);
-        const int m0 = (t_m - (g ? ends[g - 1] : 0)) * kGenM;
+        const int col0 = (int)(t % nt) * cols;
+        const Piece p = find_piece(a, ends, each, (int)(t / nt), pieces);
+        const int g = p.group;
+        const Group grp = p.rows;
+        const int m0 = p.n * kGenM;
         const int rows = min(kGenM, grp.rows - m0);
         const uint8_t* in = a.in + (grp.row + m0) * a.in_row;
         uint8_t* out = a.out + (grp.row + m0) * a.out_row;

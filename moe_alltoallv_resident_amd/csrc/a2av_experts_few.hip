@@ -19,7 +19,6 @@ constexpr int kBlocksPerCu = 2;
 constexpr int kDirectRows = 16;          // rows that the direct form takes at most
 [[maybe_unused]] constexpr int kStreamRows = 128;     // weight rows of a stream tile
 [[maybe_unused]] constexpr int kStreamLds = 79872;    // of a block: half of a CU's but for the list of groups
-[[maybe_unused]] constexpr int kCoarse = 8;               // beyond 512 groups `ends` has an entry for so many
 
 // Elements of a unit, the step of the walk along a row: 16 bytes of a weight row for each lane
 // (32 with 8-bit weights).
@@ -375,8 +374,8 @@ template <int KIND>
 __global__ void __launch_bounds__(kThreads, 2 * kBlocksPerCu) expert_few_kernel(ExpertArgs a) {
 #ifdef A2AV_DEVICE_CODE
     __shared__ __align__(1024) uint8_t lds[kStreamLds];
-    __shared__ int ends[kMaxExperts / kCoarse];
-    const int per = a.G > kMaxExperts / kCoarse ? kCoarse : 1;      // groups of an entry of `ends`
+    __shared__ int ends[kEntries];
+    const int per = groups_an_entry(a);
     const int cols_stream = a.swiglu ? kStreamRows / 2 : kStreamRows;
     const int nt_stream = (a.width + cols_stream - 1) / cols_stream;
     const int chunk = a.few;                                 // rows of a stream tile
@@ -385,17 +384,10 @@ __global__ void __launch_bounds__(kThreads, 2 * kBlocksPerCu) expert_few_kernel(
     auto pieces = [&](int rows) { return rows > lo && rows <= hi ? pieces_of(rows, chunk) : 0; };
     auto list = [&] { return __builtin_amdgcn_readfirstlane(count_tiles<kThreads>(a, ends, (int*)lds, pieces, per)); };
     auto job_at = [&](int i, int col0) {
-        const int e = __builtin_amdgcn_readfirstlane(find_group(ends, (a.G + per - 1) / per, i));
-        int left = i - (e ? __builtin_amdgcn_readfirstlane(ends[e - 1]) : 0);
-        int grp = e * per;
-        bool bad = false;
-        Group gr = group_of(a, grp, &bad);
-        // no round unless an entry has several groups
-        for (int p; grp + 1 < a.G && left >= (p = pieces(gr.rows)); gr = group_of(a, ++grp, &bad)) left -= p;
-        grp = __builtin_amdgcn_readfirstlane(grp);
-        const int64_t w0 = (int64_t)grp * a.N, row = gr.row + (int64_t)left * chunk;
+        const Piece p = find_piece(a, ends, per, i, pieces);
+        const int64_t w0 = (int64_t)p.group * a.N, row = p.rows.row + (int64_t)p.n * chunk;
         return Job{a.in + row * a.in_row, a.weight + w0 * a.w_row, a.scales + w0 * (a.K / kMxGroup), a.out + row * a.out_row,
-                   __builtin_amdgcn_readfirstlane(min(chunk, gr.rows - left * chunk)), col0};
+                   __builtin_amdgcn_readfirstlane(min(chunk, p.rows.rows - p.n * chunk)), col0};
     };
     // stream tiles of the small groups and of all, row tiles of the large ones, groups for the direct form
     const Four n4 = count_groups<kThreads>(a, (int*)lds, [&](int rows) {

@@ -3,11 +3,13 @@
 // A tile is up to 256 rows of one expert by 256 rows of its weight.  Both are staged through
 // LDS in steps of 128 bytes of a row (64 bfloat16, 128 e4m3, 32 float32 elements; 4-bit weights
 // take 32 or 64 bytes for the same elements), loaded straight from memory into LDS while the
-// step before is multiplied.  Eight wavefronts, two along the rows and four along the weight,
-// hold 128 x 64 results each in registers.  The weight is the matrix instruction's first
-// operand, so a lane ends up with four neighbouring columns of one output row.
+// steps before are multiplied.  Four wavefronts, one on each SIMD, hold 128 x 128 results each:
+// that takes 128 KB of LDS reads a step where eight wavefronts of 128 x 64 take 192 KB, which
+// with the 64 KB that arrive kept LDS busy for as long as the matrix units.  The weight is the
+// matrix instruction's first operand, so a lane ends up with four neighbouring columns of one
+// output row.
 //
-// Matrix instructions: 16x16x32 (bfloat16), 16x16x4 (float32), 16x16x128 with a scale for every
+// Matrix instructions: 32x32x16 (bfloat16), 32x32x2 (float32), 32x32x64 with a scale for every
 // 32 elements (e4m3 and E2M1 as they are stored).  4-bit weights with bfloat16 rows are widened
 // in registers, exactly: an E2M1 element times a power of two is a bfloat16.
 #include "a2av_experts.h"
@@ -15,7 +17,7 @@
 namespace a2av {
 namespace {
 
-[[maybe_unused]] constexpr int kThreads = 512, kWaves = kThreads / kWave;
+[[maybe_unused]] constexpr int kThreads = 256, kWaves = kThreads / kWave;
 constexpr int kTileN = kTileRows;        // weight rows of a tile
 constexpr int kMaxM = kTileRows;         // input rows of the largest tile
 constexpr int kRowStep = 128;            // bytes of an input row in a step
@@ -39,16 +41,12 @@ struct Scales {
     alignas(1024) uint8_t of[kTileN + kMaxM][kQuad];
 };
 
-// A wavefront's place to put output rows together, in the second half of the scales: that is free
-// while the next tile's first steps are loaded.
-[[maybe_unused]] constexpr int kOutStage = sizeof(Scales) / kWaves;
-static_assert(kOutStage == 1024, "eight rows of 128 bytes");
-
 template <int KIND>
 struct Shared {
     Stage<KIND> stage[2];
     Scales scales[2];
-    int ends[kMaxExperts];
+    int ends[kEntries];
+    uint32_t ahead[kWaves][kWave];   // what is loaded only to have it in the L2 goes here
 };
 
 // Where 16-byte piece c of row r stands in its LDS row: eight neighbouring rows' same pieces, read
@@ -68,8 +66,8 @@ __device__ inline int piece_at(int r, int p) {
     else return p;
 }
 
-// Row pieces of 16 for each of the two wavefronts along the rows: a tile has 32 * 8, 4, 2 or 1 rows.
-[[maybe_unused]] __device__ inline int height_of(int rows) { return rows > 128 ? 8 : rows > 64 ? 4 : rows > 32 ? 2 : 1; }
+// Row pieces of 32 for each of the two wavefronts along the rows: a tile has 64 * 4, 2 or 1 rows.
+[[maybe_unused]] __device__ inline int height_of(int rows) { return rows > 128 ? 4 : rows > 64 ? 2 : 1; }
 
 struct Tile {
     const uint8_t* in;       // its first row
@@ -86,21 +84,21 @@ template <int KIND>
 struct Loader {
     static constexpr int kWStep = weight_step(KIND), kWPieces = kWStep / 16, kWRows = kWave / kWPieces;
     static constexpr int kWLoads = kTileN / kWRows / kWaves;     // of a wavefront for a step
-    static constexpr int kXLoads = kMaxM / 8 / kWaves;           // load i: the tile's rows 64 i .. 64 i + 63
+    static constexpr int kXLoads = kMaxM / 8 / kWaves;           // load i: the tile's rows 32 i .. 32 i + 31
     static constexpr int kBlocks = step_elems(KIND) / kMxGroup;  // scale bytes of a step
 
     Shared<KIND>& sh;
     int lane, wave, steps, blocks;
     u32x4 xbuf, wbuf, sbuf;
-    uint32_t xo[kXLoads], wo[kWLoads], so;
+    uint32_t xo[kXLoads], wo[kWLoads], wso, xso, xrow;
     bool x_over, w_over;     // the lane's pieces are past the row's end in the last step
-    const uint8_t* sp;       // scales that are read byte by byte
+    const uint8_t *wsp, *xsp;   // scales that are read byte by byte
 
-    // weight row of tile row r: with SwiGLU 16 gate rows and the 16 up rows of the same columns in turn
+    // weight row of tile row r: with SwiGLU 32 gate rows and the 32 up rows of the same columns in turn
     static __device__ int weight_row(const ExpertArgs& a, const Tile& t, int r) {
         if (!a.swiglu) return t.col0 + r < a.width ? t.col0 + r : -1;
-        const int c = t.col0 + (r / 32) * 16 + r % 16;
-        return c < a.width ? c + (r / 16 % 2 ? a.width : 0) : -1;
+        const int c = t.col0 + (r / 64) * 32 + r % 32;
+        return c < a.width ? c + (r / 32 % 2 ? a.width : 0) : -1;
     }
 
     __device__ __forceinline__ Loader(const ExpertArgs& a, Shared<KIND>& s) : sh(s) {
@@ -128,18 +126,15 @@ struct Loader {
             const int wr = weight_row(a, t, (i * kWaves + wave) * kWRows + lane / kWPieces);
             wo[i] = wr < 0 ? kOutside : (uint32_t)(wr * a.w_row + wc);
         }
+        xrow = (uint32_t)(threadIdx.x * a.in_row);
         if constexpr (weight_scaled(KIND)) {
-            // wavefronts 0 .. 3 load the weight rows' scales, 4 .. 7 the input rows'
-            sbuf = buffer_words(wave < 4 ? t.scales : t.in,
-                                wave < 4 ? (uint32_t)a.N * (uint32_t)blocks : (uint32_t)(t.rows * a.in_row));
-            sp = wave < 4 ? t.scales : t.in;
-            so = kOutside;
-            if (wave < 4) {
-                const int wr = weight_row(a, t, threadIdx.x);
-                if (wr >= 0) so = (uint32_t)(wr * blocks);
-            } else if (rows_scaled(KIND) && (int)threadIdx.x - kTileN < t.rows) {
-                so = (uint32_t)((threadIdx.x - kTileN) * a.in_row + a.K);
-            }
+            const int wr = weight_row(a, t, threadIdx.x);
+            // each wavefront loads the scales of 64 weight rows and of 64 input rows
+            sbuf = buffer_words(t.scales, (uint32_t)a.N * (uint32_t)blocks);
+            wsp = t.scales;
+            xsp = t.in;
+            wso = wr >= 0 ? (uint32_t)(wr * blocks) : kOutside;
+            xso = (int)threadIdx.x < t.rows ? (uint32_t)(threadIdx.x * a.in_row + a.K) : kOutside;
         }
     }
     // Loads past the last step read zeros too: the counts that the waits go by stay the same.
@@ -147,225 +142,247 @@ struct Loader {
         const bool on = s < steps - 1 || (s == steps - 1 && !x_over);
         load_to_lds(xbuf, sh.stage[s & 1].x + (i * kWaves + wave) * 1024, on ? xo[i] : kOutside, s * kRowStep);
     }
-    __device__ __forceinline__ void weights(int s) {
+    __device__ __forceinline__ void weights(int s, int i) {
         const bool on = s < steps - 1 || (s == steps - 1 && !w_over);
-#pragma unroll
-        for (int i = 0; i < kWLoads; ++i)
-            load_to_lds(wbuf, sh.stage[s & 1].w + (i * kWaves + wave) * 1024, on ? wo[i] : kOutside, s * kWStep);
+        load_to_lds(wbuf, sh.stage[s & 1].w + (i * kWaves + wave) * 1024, on ? wo[i] : kOutside, s * kWStep);
+    }
+    // The memory lines of a step's input rows, into the L2 alone: a word of each of the wavefront's 64
+    // rows.  8-bit rows are not whole lines long, so most of their 128-byte pieces lie in two lines and
+    // come later than the weights' (185 -> 165 thousand cycles a tile of 40 steps).  Rows and weights
+    // in whole lines lost by it (220 -> 258 thousand a tile of 80 steps in bfloat16).
+    static constexpr int kLookAhead = rows_scaled(KIND) ? 4 : 0;   // steps
+    __device__ __forceinline__ void look_ahead(int s) {
+        if constexpr (kLookAhead > 0) load_word_to_lds(xbuf, sh.ahead[wave], s < steps ? xrow : kOutside, s * kRowStep);
+    }
+    // load n of a step's
+    __device__ __forceinline__ void load(int s, int n) {
+        if (n < kWLoads) weights(s, n);
+        else rows(s, n - kWLoads);
     }
     // Scale bytes, sixteen blocks at a time.  Rows of scales that are not whole words (a width that
     // is no multiple of 128) are read byte by byte.
     __device__ __forceinline__ void scales(const ExpertArgs& a, int quad) {
-        if (!weight_scaled(KIND) || (wave >= 4 && !rows_scaled(KIND)) || quad * kQuad >= blocks) return;
-        uint8_t* to = sh.scales[quad & 1].of[wave * kWave];
+        if (!weight_scaled(KIND) || quad * kQuad >= blocks) return;
+        uint8_t* wto = sh.scales[quad & 1].of[wave * kWave];
+        uint8_t* xto = sh.scales[quad & 1].of[kTileN + wave * kWave];
         if (blocks % 4 == 0 && (uintptr_t)a.scales % 4 == 0) {
-            load_to_lds(sbuf, to, so, quad * kQuad);
+            load_to_lds(sbuf, wto, wso, quad * kQuad);
+            if (rows_scaled(KIND)) load_to_lds(xbuf, xto, xso, quad * kQuad);
         } else {
-#pragma unroll 1
-            for (int w = 0; w < kQuad; w += 4) {
-                uint32_t v = 0;
-                for (int i = 0; i < 4; ++i)
-                    if (so != kOutside && quad * kQuad + w + i < blocks) v |= (uint32_t)sp[so + quad * kQuad + w + i] << (8 * i);
-                *(uint32_t*)(to + lane * kQuad + w) = v;
-            }
+            bytes(wto, wsp, wso, quad);
+            if (rows_scaled(KIND)) bytes(xto, xsp, xso, quad);
         }
     }
-    // What the first steps wait for, in the order of the steps that follow.
-    template <int LO, int HI>
-    __device__ __forceinline__ void first(const ExpertArgs& a) {
-        scales(a, 0);
-        weights(0);
-#pragma unroll
-        for (int i = 0; i < LO + HI; ++i) rows(0, i);
-        weights(1);
-#pragma unroll
-        for (int i = 0; i < LO; ++i) rows(1, i);
+    __device__ __forceinline__ void bytes(uint8_t* to, const uint8_t* from, uint32_t at, int quad) {
+#pragma unroll 1
+        for (int w = 0; w < kQuad; w += 4) {
+            uint32_t v = 0;
+            for (int i = 0; i < 4; ++i)
+                if (at != kOutside && quad * kQuad + w + i < blocks) v |= (uint32_t)from[at + quad * kQuad + w + i] << (8 * i);
+            *(uint32_t*)(to + lane * kQuad + w) = v;
+        }
     }
 };
 
+// A wavefront's operands of half a step: 64 bytes of 128 weight rows and of its input rows.
+template <int HT>
+struct Half {
+    u32x4 w[4][2], x[HT][2];
+};
+
+// A step's scale words of the same rows, so shifted that byte 2k is the lane's of half k.
+template <int HT>
+struct Words {
+    int w[4], x[HT];
+};
+
 // All steps of a tile, then its output.  A wavefront goes on to the next tile's loads as soon as its
-// own stores are on their way.
-// MT: the tile's height.  The wavefront along the rows wm has the 16-row pieces 2 i + wm.
+// own stores are on their way.  HT: the tile's height; the wavefront along the rows wm has the 32-row
+// pieces 2 i + wm.
 //
-// A step has two phases: the first multiplies the pieces 0 .. kLo - 1 of a wavefront's rows, the
-// second the others.  After the first phase nobody reads the step's weight rows (they stay in
-// registers) and first input rows again, so their places take those of the step after the next;
-// the other input rows' places are free after the second phase.  So every load has one and a
-// half steps' time with two stages of LDS.
-template <int KIND, int MT>
+// A step's first half is in registers when the step begins.  While it is multiplied the second half
+// is read; then nobody needs the step's place in LDS any more, which takes the step after the next,
+// and while the second half is multiplied the next step's first half is read.
+template <int KIND, int HT>
 __device__ __forceinline__ void run_tile(const ExpertArgs& a, const Tile& t, Shared<KIND>& sh) {
-    constexpr int kLo = MT > 2 ? MT / 2 : MT;
-    constexpr int kXLo = MT == 8 ? 2 : 1, kXHi = MT == 8 ? 2 : MT == 4 ? 1 : 0;   // loads of the two phases' rows
-    constexpr int kAhead = Loader<KIND>::kWLoads + kXLo + kXHi;
+    constexpr int kLoads = Loader<KIND>::kWLoads + 2 * HT;  // of a wavefront for a step
     constexpr int kWStep = weight_step(KIND), kBlocks = Loader<KIND>::kBlocks;
     Loader<KIND> ld(a, sh);
     ld.begin(a, t);
-    ld.template first<kXLo, kXHi>(a);
+    ld.scales(a, 0);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) ld.load(0, n);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) ld.load(1, n);
+#pragma unroll
+    for (int s = 2; s < Loader<KIND>::kLookAhead; ++s) ld.look_ahead(s);
     const int lane = ld.lane, wave = ld.wave, steps = ld.steps;
-    const int wm = wave / 4, wn = wave % 4, l16 = lane % 16, g = lane / 16;
+    const int wm = wave / 2, wn = wave % 2, l32 = lane % 32, h = lane / 32;
 
-    f32x4 acc[MT][4];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-
-    for (int s = 0; s < steps; ++s) {
+    // Read n of the kReads that bring half k of step s to registers.
+    constexpr int kReads = 4 + HT;
+    auto read = [&](Half<HT>& f, Words<HT>& words, int s, int k, int n) __attribute__((always_inline)) {
         const Stage<KIND>& st = sh.stage[s & 1];
         const uint8_t* sc = sh.scales[s * kBlocks / kQuad & 1].of[0] + s * kBlocks % kQuad;
-        wait_for_loads<kAhead>();                           // the first phase's rows of step s
-        block_barrier();                                    // the second phase of step s - 1 has been read
-#pragma unroll
-        for (int i = 0; i < kXHi; ++i) ld.rows(s + 1, kXLo + i);
-        // 16-bit and 32-bit elements: two times 64 bytes of each row; 8 and 4 bits: 128 elements at once
-        constexpr bool kScaledForm = KIND == kMx8 || KIND == kMx8Mx4;
-        u32x4 w[2][4];
-        int sw[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = wn * 64 + j * 16 + l16;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                if constexpr (KIND == kBf16Mx4) {
-                    const uint32_t q = *(const uint32_t*)(st.w + r * kWStep + k * 16 + g * 4);
-                    w[k][j] = widen_e2m1(q, __uint_as_float((uint32_t)sc[r * kQuad + k] << 23));
-                } else if constexpr (KIND == kMx8Mx4) {
-                    w[k][j] = k ? u32x4{0, 0, 0, 0} : *(const u32x4*)(st.w + place<kWStep>(r, g));
-                } else {
-                    w[k][j] = *(const u32x4*)(st.w + place<kWStep>(r, k * 4 + g));
-                }
-            }
-            if constexpr (kScaledForm) sw[j] = sc[r * kQuad + g];
-        }
-        auto multiply = [&](int i) __attribute__((always_inline)) {
-            const int r = (2 * i + wm) * 16 + l16;
-            const u32x4 x0 = *(const u32x4*)(st.x + place<128>(r, g)), x1 = *(const u32x4*)(st.x + place<128>(r, 4 + g));
-            if constexpr (kScaledForm) {
-                const int sx = sc[(kTileN + r) * kQuad + g];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = multiply_scaled<KIND>(w[0][j], w[1][j], sw[j], x0, x1, sx, acc[i][j]);
+        if (n < 4) {
+            const int r = wn * 128 + n * 32 + l32;
+            if constexpr (KIND == kBf16Mx4) {
+                const float scale = __uint_as_float((uint32_t)sc[r * kQuad + k] << 23);
+                f.w[n][0] = widen_e2m1(*(const uint32_t*)(st.w + r * kWStep + k * 16 + h * 4), scale);
+                f.w[n][1] = widen_e2m1(*(const uint32_t*)(st.w + r * kWStep + k * 16 + 8 + h * 4), scale);
+            } else if constexpr (KIND == kMx8Mx4) {
+                f.w[n][0] = *(const u32x4*)(st.w + place<kWStep>(r, k * 2 + h));
+                f.w[n][1] = u32x4{0, 0, 0, 0};
             } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = multiply16<KIND>(w[0][j], x0, acc[i][j]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = multiply16<KIND>(w[1][j], x1, acc[i][j]);
+                f.w[n][0] = *(const u32x4*)(st.w + place<kWStep>(r, k * 4 + h));
+                f.w[n][1] = *(const u32x4*)(st.w + place<kWStep>(r, k * 4 + 2 + h));
             }
-        };
-#pragma unroll
-        for (int i = 0; i < kLo; ++i) multiply(i);
-        wait_for_loads<kAhead>();                           // the second phase's rows of step s
-        block_barrier();                                    // the first phase's have been read
-        ld.weights(s + 2);
-#pragma unroll
-        for (int i = 0; i < kXLo; ++i) ld.rows(s + 2, i);
-        if (s * kBlocks % kQuad == 0) ld.scales(a, s * kBlocks / kQuad + 1);
-#pragma unroll
-        for (int i = kLo; i < MT; ++i) multiply(i);
-    }
-    block_barrier();                                        // the last step has been read
-
-    // Results: lane (l16, g) has columns 4g .. 4g + 3 of a 16 x 16 piece, of input row l16.  Stored
-    // as they are, every row would go out in pieces of 32 bytes; so a wavefront puts up to 128 bytes
-    // of 8 or 16 rows together in LDS first.
-    uint8_t* stage = (uint8_t*)&sh.scales[1] + wave * kOutStage;
-    const bool mx_out = rows_scaled(KIND) && a.out_dtype == A2AV_MX8;
-    const bool runs = mx_out || (a.out_row % 16 == 0 && (uintptr_t)a.out % 16 == 0);
-    const int c0 = t.col0 + wn * (a.swiglu ? 32 : 64);      // the wavefront's first column
-    // Writes `rows` staged rows of `bytes` bytes, the first of them the tile's row r0, to column c.
-    auto write = [&](int r0, int rows, int bytes, int c, int elem) __attribute__((always_inline)) {
-        const int pieces = bytes / 16;
-        const int r = lane / pieces, p = lane % pieces;
-        wave_sync();
-        const u32x4 v = r < rows ? *(const u32x4*)(stage + r * bytes + p * 16) : u32x4{0, 0, 0, 0};
-        wave_sync();
-        const int left = (a.width - c) * elem - p * 16;     // bytes from the piece to the row's end
-        if (r < rows && r0 + r < t.rows && left > 0) {
-            uint8_t* to = t.out + (r0 + r) * a.out_row + (int64_t)c * elem + p * 16;
-            if (runs && left >= 16) {
-                *(u32x4*)to = v;
-            } else if constexpr (KIND == kF32) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (4 * e < left) ((uint32_t*)to)[e] = v[e];
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (2 * e < left) ((u16*)to)[e] = (u16)(v[e / 2] >> (16 * (e % 2)));
-            }
+            if (k == 0) words.w[n] = rows_scaled(KIND) ? *(const uint32_t*)(sc + r * kQuad) >> (8 * h) : 0;
+        } else {
+            const int i = n - 4, r = (2 * i + wm) * 32 + l32;
+            f.x[i][0] = *(const u32x4*)(st.x + place<128>(r, k * 4 + h));
+            f.x[i][1] = *(const u32x4*)(st.x + place<128>(r, k * 4 + 2 + h));
+            if (k == 0) words.x[i] = rows_scaled(KIND) ? *(const uint32_t*)(sc + (kTileN + r) * kQuad) >> (8 * h) : 0;
         }
     };
-    auto pair = [](float lo, float hi) { return f32_to_bf16(lo) | f32_to_bf16(hi) << 16; };
+    f32x16 acc[HT][4];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int r0 = (2 * i + wm) * 16;
-        if (r0 >= t.rows) continue;
-        f32x4 v[4];
-        if (a.swiglu) {
+    for (int i = 0; i < HT; ++i)
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[p][e] = silu_mul(acc[i][2 * p][e], acc[i][2 * p + 1][e]);
-            v[2] = v[3] = f32x4{0, 0, 0, 0};
-        } else {
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    // Product n of a half.  The order of reads, loads and products is fixed piece by piece: left to
+    // itself the compiler puts every read right before its use, and with one wavefront on a SIMD
+    // nothing else runs while it waits.
+    constexpr int kProducts = 4 * HT;
+    auto multiply = [&](const Half<HT>& f, const Words<HT>& words, auto half, int n) __attribute__((always_inline)) {
+        const int i = n / 4, j = n % 4;
+        acc[i][j] = multiply32<KIND, 2 * decltype(half)::value>(f.w[j][0], f.w[j][1], words.w[j], f.x[i][0], f.x[i][1], words.x[i],
+                                                                acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    constexpr std::integral_constant<int, 0> kFirst{};
+    constexpr std::integral_constant<int, 1> kSecond{};
+
+    Half<HT> f0, f1;
+    Words<HT> words, next;
+    wait_for_loads<kLoads + (Loader<KIND>::kLookAhead ? Loader<KIND>::kLookAhead - 2 : 0)>();   // step 0; step 1 is on its way
+    block_barrier();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = acc[i][j];
+    for (int n = 0; n < kReads; ++n) read(f0, next, 0, 0, n);
+    for (int s = 0; s < steps; ++s) {
+        words = next;
+#pragma unroll
+        for (int n = 0; n < kProducts; ++n) {
+#pragma unroll
+            for (int q = n * kReads / kProducts; q < (n + 1) * kReads / kProducts; ++q) read(f1, words, s, 1, q);
+            multiply(f0, words, kFirst, n);
         }
-        if (rows_scaled(KIND) && mx_out) {
-            const int bytes = a.swiglu ? 32 : 64;
-            // 32 columns: two pieces of the four lanes that share a row
+        wait_for_loads<Loader<KIND>::kLookAhead ? 1 : 0>(); // step s + 1; what is looked ahead for may be on its way
+        block_barrier();                                    // for everyone; step s has been read
+        if (s * kBlocks % kQuad == 0) ld.scales(a, s * kBlocks / kQuad + 1);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (h == 1 && a.swiglu) continue;
-                uint32_t m = 0;
+        for (int n = 0; n < kProducts; ++n) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) m = max(m, max(abs_bits(v[2 * h][e]), abs_bits(v[2 * h + 1][e])));
-                m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-                m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-                const uint32_t sb = mx_scale_byte(m);
-                const float f = mx_inverse(sb);
+            for (int q = n * kLoads / kProducts; q < (n + 1) * kLoads / kProducts; ++q) ld.load(s + 2, q);
+            if (n == kProducts - 1) ld.look_ahead(s + Loader<KIND>::kLookAhead);
 #pragma unroll
-                for (int q = 2 * h; q < 2 * h + 2; ++q)
-                    *(uint32_t*)(stage + l16 * bytes + 16 * q + 4 * g) = mx8_pack(v[q][0] * f, v[q][1] * f, v[q][2] * f,
-                                                                                  v[q][3] * f, sb == 255u);
-                const int c = c0 + 32 * h;                  // the width is a multiple of 32
-                if (r0 + l16 < t.rows && c < a.width) {
-                    uint8_t* row = t.out + (r0 + l16) * a.out_row;
-                    if (g == 0) row[a.width + c / kMxGroup] = (uint8_t)sb;
-                    if (c + 32 == a.width)
-                        for (int b = a.width + a.width / kMxGroup + g; b < a.out_row; b += 4) row[b] = 0;
-                }
-            }
-            write(r0, 16, bytes, c0, 1);
-        } else if constexpr (KIND == kF32) {
-#pragma unroll
-            for (int q = 0; q < 4; q += 2) {                // 32 columns at a time, 8 rows at a time
-                if (q == 2 && a.swiglu) continue;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (l16 / 8 == half) {
-                        *(f32x4*)(stage + l16 % 8 * 128 + 16 * g) = v[q];
-                        *(f32x4*)(stage + l16 % 8 * 128 + 64 + 16 * g) = v[q + 1];
-                    }
-                    write(r0 + 8 * half, 8, 128, c0 + 16 * q, 4);
-                }
-            }
-        } else if (a.swiglu) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-                *(u32x2*)(stage + l16 * 64 + 32 * q + 8 * g) = u32x2{pair(v[q][0], v[q][1]), pair(v[q][2], v[q][3])};
-            write(r0, 16, 64, c0, 2);
-        } else {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (l16 / 8 == half) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        *(u32x2*)(stage + l16 % 8 * 128 + 32 * q + 8 * g) = u32x2{pair(v[q][0], v[q][1]), pair(v[q][2], v[q][3])};
-                }
-                write(r0 + 8 * half, 8, 128, c0, 2);
-            }
+            for (int q = n * kReads / kProducts; q < (n + 1) * kReads / kProducts; ++q) read(f0, next, s + 1, 0, q);   // zeros after the last step
+            multiply(f1, words, kSecond, n);
         }
     }
+    wait_for_loads<0>();
+    block_barrier();                                        // the last step has been read
+
+    // Results: lane (l32, h) has columns 8q + 4h .. 8q + 4h + 3 of a 32 x 32 piece, of input row l32.
+    // They go through the wavefront's quarter of the stages in float32, and a short loop makes eight
+    // output columns a lane of them, in runs of up to 256 bytes a row.  (Done in registers instead, the
+    // same work is unrolled for every piece and form of output: that code no longer fits the
+    // instruction cache and took four times as long.)
+    constexpr int kRoom = sizeof(sh.stage) / kWaves / 1024 * 1024;
+    constexpr int kPitch = 128 * 4, kFit = kRoom / (32 * kPitch) < HT ? kRoom / (32 * kPitch) : HT;   // 32-row pieces at a time
+    static_assert(kFit >= 1 && HT % kFit == 0, "whole passes");
+    uint8_t* stage = (uint8_t*)&sh.stage[0] + wave * kRoom;
+    auto at = [&](int r, int piece) { return (f32x4*)(stage + r * kPitch + ((piece ^ (r & 15)) << 4)); };   // four columns
+    const bool mx_out = rows_scaled(KIND) && a.out_dtype == A2AV_MX8;
+    const int elem = mx_out ? 1 : KIND == kF32 ? 4 : 2;
+    const int shift = a.swiglu ? 3 : 4;                     // 8 or 16 times eight columns of the wavefront
+    const int c0 = t.col0 + (wn << (shift + 3));
+    const bool runs = mx_out || (a.out_row % 16 == 0 && (uintptr_t)a.out % 16 == 0);
+#pragma unroll
+    for (int i0 = 0; i0 < HT; i0 += kFit) {
+#pragma unroll
+        for (int i = i0; i < i0 + kFit; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *at((i - i0) * 32 + l32, j * 8 + 2 * q + h) = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                                                                        acc[i][j][4 * q + 3]};
+        wave_sync();
+#pragma unroll 1
+        for (int n = lane; n < kFit * 32 << shift; n += kWave) {
+            const int r = n >> shift, u = n & ((1 << shift) - 1), row = (2 * (i0 + r / 32) + wm) * 32 + r % 32, c = c0 + 8 * u;
+            f32x4 lo, hi;
+            if (a.swiglu) {
+                const int gate = u / 4 * 16 + u % 4 * 2;
+                lo = *at(r, gate);
+                hi = *at(r, gate + 1);
+                const f32x4 ulo = *at(r, gate + 8), uhi = *at(r, gate + 9);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    lo[e] = silu_mul(lo[e], ulo[e]);
+                    hi[e] = silu_mul(hi[e], uhi[e]);
+                }
+            } else {
+                lo = *at(r, 2 * u);
+                hi = *at(r, 2 * u + 1);
+            }
+            const int left = (a.width - c) * elem;          // bytes to the row's end
+            const bool on = row < t.rows && left > 0;
+            uint8_t* to = t.out + row * a.out_row + (int64_t)c * elem;
+            if (rows_scaled(KIND) && mx_out) {
+                // a scale's 32 columns are four neighbouring lanes' (the width is a multiple of 32)
+                uint32_t m = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m = max(m, max(abs_bits(lo[e]), abs_bits(hi[e])));
+                m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+                m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+                const uint32_t sb = mx_scale_byte(m);
+                const float f = mx_inverse(sb);
+                if (!on) continue;
+                *(u32x2*)to = u32x2{mx8_pack(lo[0] * f, lo[1] * f, lo[2] * f, lo[3] * f, sb == 255u),
+                                    mx8_pack(hi[0] * f, hi[1] * f, hi[2] * f, hi[3] * f, sb == 255u)};
+                if (u % 4 == 0) t.out[row * a.out_row + a.width + c / kMxGroup] = (uint8_t)sb;
+                if (c + 8 == a.width)
+                    for (int b = a.width + a.width / kMxGroup; b < a.out_row; ++b) t.out[row * a.out_row + b] = 0;
+            } else if constexpr (KIND == kF32) {
+                if (!on) continue;
+                if (runs && left >= 32) {
+                    ((f32x4*)to)[0] = lo;
+                    ((f32x4*)to)[1] = hi;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (4 * e < left) ((float*)to)[e] = e < 4 ? lo[e % 4] : hi[e % 4];
+                }
+            } else {
+                if (!on) continue;
+                const u32x4 v = {f32_to_bf16_pair(lo[0], lo[1]), f32_to_bf16_pair(lo[2], lo[3]), f32_to_bf16_pair(hi[0], hi[1]),
+                                 f32_to_bf16_pair(hi[2], hi[3])};
+                if (runs && left >= 16) {
+                    *(u32x4*)to = v;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (2 * e < left) ((u16*)to)[e] = (u16)(v[e / 2] >> (16 * (e % 2)));
+                }
+            }
+        }
+        wave_sync();
+    }
+    block_barrier();                                        // the stages are free
 }
 #endif
 
@@ -373,9 +390,9 @@ template <int KIND>
 __global__ void __launch_bounds__(kThreads) expert_tile_kernel(ExpertArgs a) {
 #ifdef A2AV_DEVICE_CODE
     __shared__ Shared<KIND> sh;
-    int* ends = sh.ends;
-    const int mt = __builtin_amdgcn_readfirstlane(count_tiles<kThreads>(
-        a, ends, (int*)sh.stage[0].x, [&](int rows) { return rows > a.few ? pieces_of(rows, kMaxM) : 0; }));
+    auto pieces = [&](int rows) { return rows > a.few ? pieces_of(rows, kMaxM) : 0; };
+    const int each = groups_an_entry(a);
+    const int mt = __builtin_amdgcn_readfirstlane(count_tiles<kThreads>(a, sh.ends, (int*)sh.stage[0].x, pieces, each));
     const int cols = a.swiglu ? kTileN / 2 : kTileN;
     const int nt = (a.width + cols - 1) / cols;
     const int64_t total = (int64_t)mt * nt;
@@ -391,17 +408,14 @@ __global__ void __launch_bounds__(kThreads) expert_tile_kernel(ExpertArgs a) {
         const int in_sup = (int)(t - sup * kSuper * nt), high = min(kSuper, mt - (int)sup * kSuper);
         const int tm = __builtin_amdgcn_readfirstlane((int)sup * kSuper + in_sup % high);
         const int tn = __builtin_amdgcn_readfirstlane(in_sup / high);
-        const int grp = __builtin_amdgcn_readfirstlane(find_group(ends, a.G, tm));
-        bool bad = false;
-        const Group gr = group_of(a, grp, &bad);
-        const int m0 = (tm - (grp ? __builtin_amdgcn_readfirstlane(ends[grp - 1]) : 0)) * kMaxM;
-        const int64_t row = gr.row + m0;
-        const int64_t w0 = (int64_t)grp * a.N;
+        const Piece p = find_piece(a, sh.ends, each, tm, pieces);
+        const int m0 = p.n * kMaxM;
+        const int64_t row = p.rows.row + m0, w0 = (int64_t)p.group * a.N;
         tile.in = a.in + row * a.in_row;
         tile.weight = a.weight + w0 * a.w_row;
         tile.scales = a.scales + w0 * (a.K / kMxGroup);
         tile.out = a.out + row * a.out_row;
-        tile.rows = __builtin_amdgcn_readfirstlane(min(kMaxM, gr.rows - m0));
+        tile.rows = __builtin_amdgcn_readfirstlane(min(kMaxM, p.rows.rows - m0));
         tile.col0 = tn * cols;
         return tile;
     };
@@ -409,7 +423,6 @@ __global__ void __launch_bounds__(kThreads) expert_tile_kernel(ExpertArgs a) {
     for (int64_t t = pos; tile.rows > 0; t += gridDim.x) {
         const Tile next = tile_at(t + gridDim.x);
         switch (height_of(tile.rows)) {
-            case 8: run_tile<KIND, 8>(a, tile, sh); break;
             case 4: run_tile<KIND, 4>(a, tile, sh); break;
             case 2: run_tile<KIND, 2>(a, tile, sh); break;
             default: run_tile<KIND, 1>(a, tile, sh); break;

@@ -26,6 +26,13 @@ __device__ inline float bf16_to_f32(uint32_t v) { return __uint_as_float(v << 16
 // Round to bfloat16, nearest, ties to even; NaN stays NaN.
 __device__ inline uint32_t f32_to_bf16(float f) { return __builtin_bit_cast(u16, (__bf16)f); }
 
+// Two of them in one instruction, the first in the low half.
+__device__ inline uint32_t f32_to_bf16_pair(float a, float b) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+
 // Magnitude bits: as unsigned integers they order like the magnitudes, with NaN above
 // infinity above every number, so an integer maximum keeps a NaN.
 __device__ inline uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7FFFFFFFu; }
