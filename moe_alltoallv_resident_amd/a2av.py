@@ -5,8 +5,8 @@ raw device addresses as ints) where the C call takes device pointers; the stream
 defaults to torch's current stream.  No step of the path runs in Python: the library is
 required, and a missing build raises at import of the first call.
 """
-import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -262,32 +262,48 @@ def a2av_timing_end(h):
     return list(ms), list(n)
 
 
-def _same_device(named):
-    # host-side checks only, as Session's: every tensor a contiguous GPU tensor of one device
-    device = None
-    for name, t in named:
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch tensor")
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous GPU tensor")
-        if device is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
-        device = t.device
-    return device
+# The checks below are host-side only (no synchronisation), as Session's, and written for small
+# calls, where they take longer than the kernels.
+
+def _check_device(name, t, dev):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if dev < 0 or t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}: every tensor must be on one GPU")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _need(name, t, dtype, shape):
+def _check_like(name, t, dev, dtype, shape):
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+        _check_device(name, t, dev)
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _on(device):
-    # the library launches on the current GPU
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+# the current stream's address without the Stream object around it, where torch offers that
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _launch(name, dev, stream, call):
+    """call(stream) with `dev` the current GPU, on the given stream or that GPU's current one."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(name, dev, stream, call)
+    if stream is None:
+        stream = _current_stream(dev)
+    rc = call(stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream)
+    if rc != OK:
+        raise A2AVError(name, rc)
+
+
+_ROWS_DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 def rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, y8=None, stream=None) -> None:
@@ -297,40 +313,63 @@ def rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, y8=None, s
     [..., a2av_row_bytes(MX8, hidden)].  weight may be None (ones).  The outputs given are
     written; at least one is.
     """
-    device = _same_device((("x", x), ("weight", weight), ("residual", residual), ("residual_out", residual_out),
-                           ("y", y), ("y8", y8)))
-    if x.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"x has dtype {x.dtype}, expected float32 or bfloat16")
-    if x.dim() < 1:
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch tensor")
+    dtype, shape, dev = x.dtype, x.shape, x.get_device()
+    code = _ROWS_DTYPE.get(dtype)
+    if code is None:
+        raise TypeError(f"x has dtype {dtype}, expected float32 or bfloat16")
+    if not shape:
         raise ValueError("x must have at least one dimension")
-    hidden = x.shape[-1]
+    hidden = shape[-1]
+    _check_device("x", x, dev)
     if weight is not None:
-        _need("weight", weight, x.dtype, (hidden,))
-    for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
-        if t is not None:
-            _need(name, t, x.dtype, x.shape)
+        _check_like("weight", weight, dev, dtype, (hidden,))
+    if residual is not None:
+        _check_like("residual", residual, dev, dtype, shape)
+    if residual_out is not None:
+        _check_like("residual_out", residual_out, dev, dtype, shape)
+    if y is not None:
+        _check_like("y", y, dev, dtype, shape)
     if y8 is not None:
-        _need("y8", y8, torch.uint8, x.shape[:-1] + (a2av_row_bytes(MX8, hidden),))
+        _check_like("y8", y8, dev, torch.uint8, shape[:-1] + (a2av_row_bytes(MX8, hidden),))
     rows = x.numel() // hidden if hidden else 0
-    with _on(device):
-        a2av_rmsnorm(x, residual, weight, residual_out, y, y8, rows, hidden,
-                     F32 if x.dtype == torch.float32 else BF16, eps, stream)
+    _launch("a2av_rmsnorm", dev, stream, lambda st: lib().a2av_rmsnorm(
+        x.data_ptr(), _address(residual), _address(weight), _address(residual_out), _address(y), _address(y8), rows, hidden,
+        code, eps, st))
 
 
-def _matmul_config(R, epr, cap, inp, weight, out, weight_scales, in_dtype, weight_dtype, out_dtype, activation) -> Matmul:
+@functools.lru_cache(maxsize=1024)
+def _matmul_plan(R, epr, cap, k, n, in_dtype, weight_dtype, out_dtype, activation):
+    """The call's description and the row lengths (in elements of the tensors) that it asks for."""
     for name, d in (("in_dtype", in_dtype), ("weight_dtype", weight_dtype), ("out_dtype", out_dtype)):
         if d not in TORCH_DTYPE or (d == MX4 and name != "weight_dtype"):
             raise ValueError(f"{name} {d} is not an element type of this argument")
+    width = n // 2 if activation == ACT_SWIGLU else n
+    return (ctypes.byref(Matmul(R, epr, cap, k, n, in_dtype, weight_dtype, out_dtype, activation)),
+            (R, cap, a2av_row_bytes(MX8, k) if in_dtype == MX8 else k),
+            (R, cap, a2av_row_bytes(MX8, width) if out_dtype == MX8 else width))
+
+
+def _expert_matmul(dev, R, epr, cap, inp, offsets, weight, out, status, weight_scales, in_dtype, weight_dtype, out_dtype,
+                   activation, stream):
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError("weight must be a torch tensor")
     if weight.dim() != 3:
         raise ValueError(f"weight has {weight.dim()} dimensions, expected 3")
-    n, k = weight.shape[1], weight.shape[2] * (2 if weight_dtype == MX4 else 1)
-    width = n // 2 if activation == ACT_SWIGLU else n
-    _need("weight", weight, TORCH_DTYPE[weight_dtype], (R * epr, n, weight.shape[2]))
-    _need("inp", inp, TORCH_DTYPE[in_dtype], (R, cap, a2av_row_bytes(MX8, k) if in_dtype == MX8 else k))
-    _need("out", out, TORCH_DTYPE[out_dtype], (R, cap, a2av_row_bytes(MX8, width) if out_dtype == MX8 else width))
+    _, n, w_row = weight.shape
+    k = w_row * 2 if weight_dtype == MX4 else w_row
+    cfg, in_shape, out_shape = _matmul_plan(R, epr, cap, k, n, in_dtype, weight_dtype, out_dtype, activation)
+    _check_like("weight", weight, dev, TORCH_DTYPE[weight_dtype], (R * epr, n, w_row))
+    _check_like("inp", inp, dev, TORCH_DTYPE[in_dtype], in_shape)
+    _check_like("out", out, dev, TORCH_DTYPE[out_dtype], out_shape)
     if weight_scales is not None:
-        _need("weight_scales", weight_scales, torch.uint8, (R * epr, n, k // 32))
-    return Matmul(R, epr, cap, k, n, in_dtype, weight_dtype, out_dtype, activation)
+        _check_like("weight_scales", weight_scales, dev, torch.uint8, (R * epr, n, k // 32))
+    _check_device("status", status, dev)
+    if status.dtype != torch.int32 or status.numel() < 1:
+        raise TypeError("status must be an int32 tensor of one element")
+    _launch("a2av_expert_matmul", dev, stream, lambda st: lib().a2av_expert_matmul(
+        cfg, inp.data_ptr(), offsets, weight.data_ptr(), _address(weight_scales), out.data_ptr(), status.data_ptr(), st))
 
 
 def expert_matmul(inp, expert_offsets, weight, out, status, weight_scales=None, in_dtype=BF16, weight_dtype=BF16,
@@ -341,17 +380,15 @@ def expert_matmul(inp, expert_offsets, weight, out, status, weight_scales=None, 
     expert_offsets int32 [R][epr + 1]; weight [R * epr][n][k] (MX4: uint8 [..][k / 2]; MX8:
     uint8); weight_scales uint8 [R * epr][n][k / 32] for MX4 and MX8; status int32 [1].
     """
-    device = _same_device((("inp", inp), ("expert_offsets", expert_offsets), ("weight", weight), ("out", out),
-                           ("status", status), ("weight_scales", weight_scales)))
+    if not isinstance(inp, torch.Tensor) or not isinstance(expert_offsets, torch.Tensor):
+        raise TypeError("inp and expert_offsets must be torch tensors")
     if expert_offsets.dim() != 2 or inp.dim() != 3:
         raise ValueError("expert_offsets must be [R][epr + 1] and inp [R][cap][row]")
-    _need("expert_offsets", expert_offsets, torch.int32, (inp.shape[0], expert_offsets.shape[1]))
-    cfg = _matmul_config(inp.shape[0], expert_offsets.shape[1] - 1, inp.shape[1], inp, weight, out, weight_scales,
-                         in_dtype, weight_dtype, out_dtype, activation)
-    if status.dtype != torch.int32 or status.numel() < 1:
-        raise TypeError("status must be an int32 tensor of one element")
-    with _on(device):
-        a2av_expert_matmul(cfg, inp, expert_offsets, weight, weight_scales, out, status, stream)
+    R, starts = expert_offsets.shape
+    dev = inp.get_device()
+    _check_like("expert_offsets", expert_offsets, dev, torch.int32, (inp.shape[0], starts))
+    _expert_matmul(dev, R, starts - 1, inp.shape[1], inp, expert_offsets.data_ptr(), weight, out, status, weight_scales,
+                   in_dtype, weight_dtype, out_dtype, activation, stream)
 
 
 class Session:
@@ -427,16 +464,11 @@ class Session:
                       activation=ACT_NONE, stream=None):
         """The experts' products on rows of the latest dispatch (expert-major sessions): inp and out are
         [R][cap][row], the group starts are the handle's own table."""
-        in_dtype = self.dtype if in_dtype is None else in_dtype
         if self.recv_layout != LAYOUT_EXPERT_MAJOR:
             raise ValueError("expert_matmul needs an expert-major session")
-        device = _same_device((("inp", inp), ("weight", weight), ("out", out), ("weight_scales", weight_scales),
-                               ("status", self.status)))
-        cfg = _matmul_config(self.R, self.epr, self.cap, inp, weight, out, weight_scales, in_dtype, weight_dtype,
-                             out_dtype, activation)
-        with _on(device):
-            a2av_expert_matmul(cfg, inp, a2av_recv_expert_offsets(self.handle), weight, weight_scales, out, self.status,
-                               stream)
+        _expert_matmul(self.status.get_device(), self.R, self.epr, self.cap, inp, a2av_recv_expert_offsets(self.handle), weight,
+                       out, self.status, weight_scales, self.dtype if in_dtype is None else in_dtype, weight_dtype, out_dtype,
+                       activation, stream)
         return out
 
     def positions(self):

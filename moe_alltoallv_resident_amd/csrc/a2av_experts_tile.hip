@@ -21,7 +21,7 @@ namespace {
 constexpr int kTileN = kTileRows;        // weight rows of a tile
 constexpr int kMaxM = kTileRows;         // input rows of the largest tile
 constexpr int kRowStep = 128;            // bytes of an input row in a step
-[[maybe_unused]] constexpr int kSuper = 8;                // row tiles that are walked together
+[[maybe_unused]] constexpr int kSuper = 4;                // row tiles that are walked together
 
 [[maybe_unused]] __host__ __device__ constexpr int weight_step(int kind) {        // bytes of a weight row in a step
     return kind == kBf16Mx4 ? 32 : kind == kMx8Mx4 ? 64 : 128;
