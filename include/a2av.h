@@ -323,7 +323,9 @@ typedef struct {
  *     (k a multiple of 32), NULL otherwise;
  * out (device) [R][capacity][a2av_row_bytes(out_dtype, n or n/2)]; it may overlap no other
  *     array.  status (device) is OR-ed.
- * 8-bit rows and 4- and 8-bit weights are 16-byte aligned.  No workspace; it can be captured
+ * 8-bit rows and 4- and 8-bit weights are 16-byte aligned; an expert's weight is below 2 GiB.
+ * float32 and bfloat16 rows may have any length and address, but multiples of 16 bytes are
+ * faster.  No workspace; it can be captured
  * in a hipGraph.  Errors: A2AV_ERR_INVALID, A2AV_ERR_HIP. */
 int a2av_expert_matmul(const a2av_matmul_t* cfg, const void* in, const int32_t* expert_offsets, const void* weight,
                        const void* weight_scales, void* out, uint32_t* status, void* stream);

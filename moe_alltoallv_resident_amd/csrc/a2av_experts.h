@@ -322,14 +322,12 @@ __device__ inline f32x4 multiply_scaled(u32x4 wlo, u32x4 whi, int ws, u32x4 xlo,
 }
 #endif
 
-// Whether the matrix-unit kernels take the call: rows and weights in whole 16-byte pieces, an
-// expert's weight and a tile's rows within 32-bit offsets.
-inline bool experts_mfma_takes(const ExpertArgs& a) {
-    return a.in_row % 16 == 0 && a.w_row % 16 == 0 && (uintptr_t)a.in % 16 == 0 && (uintptr_t)a.weight % 16 == 0 &&
-           a.N * a.w_row <= INT32_MAX && 256 * a.in_row <= INT32_MAX;
+// Whether rows and weights are whole 16-byte pieces, which the stream and tile kernels need.
+inline bool experts_whole_pieces(const ExpertArgs& a) {
+    return a.in_row % 16 == 0 && a.w_row % 16 == 0 && (uintptr_t)a.in % 16 == 0 && (uintptr_t)a.weight % 16 == 0;
 }
 
-// The general kernel, for whatever the others do not take.
+// Rows that are not (float32 and bfloat16 only: the others always are).
 hipError_t launch_experts_general(const ExpertArgs& a, int num_cu, hipStream_t st);
 // Groups of 1 .. a.few rows; of more as well, in pieces of a.few, where they would make tiles for
 // fewer than half of the CUs (a.tile_least).

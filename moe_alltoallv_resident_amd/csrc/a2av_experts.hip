@@ -5,7 +5,7 @@
 // No host knows how many rows an expert got, so no grid can be cut to them: every block
 // reads the group starts, counts the row tiles of every expert into LDS and walks the tile
 // list (tile t, t + blocks, ...) until it ends.
-// Here: the entry point and the general kernel.
+// Here: the entry point, and the kernel for rows that are not whole 16-byte pieces.
 #include "a2av_experts.h"
 
 namespace a2av {
@@ -13,112 +13,119 @@ namespace {
 
 constexpr int32_t kMaxDim = 1 << 20;
 
-// ---- the general form ----------------------------------------------------------------
-// Any width, stride and alignment that the call allows: elements are read one by one,
-// widened to float32 and multiplied on the vector units.
+// ---- rows that are not whole 16-byte pieces ------------------------------------------
+// float32 and bfloat16 rows of any length and address.  64 input rows by 64 weight rows a tile,
+// 128 bytes of each a step: through registers into LDS, 16 bytes at a time wherever the row's
+// elements lie (the memory takes such loads at any address), the last ones of a row element by
+// element.  The next step's loads run while a step is multiplied.
 
-__device__ inline float load_in(const ExpertArgs& a, const uint8_t* row, int k) {
-    if (a.in_dtype == A2AV_F32) return ((const float*)row)[k];
-    if (a.in_dtype == A2AV_BF16) return bf16_to_f32(((const u16*)row)[k]);
-    return e4m3_to_f32(row[k]) * mx_scale(row[a.K + k / kMxGroup]);
+[[maybe_unused]] constexpr int kGenThreads = 256;
+[[maybe_unused]] constexpr int kGenRows = 64;             // input rows and weight rows of a tile
+
+#ifdef A2AV_DEVICE_CODE
+// The 16 bytes at `at` of a row of `bytes` bytes, zeros past its end.
+template <typename T>
+__device__ inline u32x4 row_piece(const uint8_t* row, int at, int bytes) {
+    u32x4 v = {0, 0, 0, 0};
+    if (at + 16 <= bytes) {
+        __builtin_memcpy(&v, row + at, 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; e += sizeof(T))
+            if (at + e < bytes) v[e / 4] |= (uint32_t) * (const T*)(row + at + e) << (8 * (e % 4));
+    }
+    return v;
 }
+#endif
 
-__device__ inline float load_weight(const ExpertArgs& a, int64_t row, int k) {
-    const uint8_t* p = a.weight + row * a.w_row;
-    if (a.w_dtype == A2AV_F32) return ((const float*)p)[k];
-    if (a.w_dtype == A2AV_BF16) return bf16_to_f32(((const u16*)p)[k]);
-    const float s = mx_scale(a.scales[row * (a.K / kMxGroup) + k / kMxGroup]);
-    if (a.w_dtype == A2AV_MX8) return e4m3_to_f32(p[k]) * s;
-    return e2m1_to_f32((p[k / 2] >> (k % 2 * 4)) & 15u) * s;
-}
-
-constexpr int kGenThreads = 256;
-constexpr int kGenM = 32, kGenN = 64, kGenK = 32;   // rows, weight rows and elements of a step
-
+template <int KIND>
 __global__ void __launch_bounds__(kGenThreads) expert_general_kernel(ExpertArgs a) {
+#ifdef A2AV_DEVICE_CODE
+    using T = typename std::conditional<KIND == kF32, uint32_t, u16>::type;   // an element's bits
     __shared__ int ends[kEntries];
     __shared__ int wave_sum[kGenThreads / kWave];
-    __shared__ float xs[kGenM][kGenK + 1];
-    __shared__ float ws[kGenN][kGenK + 1];
-    __shared__ float res[kGenM][kGenN + 1];
-    auto pieces = [](int rows) { return pieces_of(rows, kGenM); };
+    __shared__ __align__(16) uint8_t xs[kGenRows * 128], ws[kGenRows * 128];
+    auto pieces = [](int rows) { return pieces_of(rows, kGenRows); };
     const int each = groups_an_entry(a);
     const int mt = count_tiles<kGenThreads>(a, ends, wave_sum, pieces, each);
-    const int cols = a.swiglu ? kGenN / 2 : kGenN;       // output columns of a tile
+    const int cols = a.swiglu ? kGenRows / 2 : kGenRows;     // output columns of a tile
     const int nt = (a.width + cols - 1) / cols;
-    const int tm = threadIdx.x / 16 * 2, tn = threadIdx.x % 16 * 4;
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, l16 = lane % 16, g = lane / 16;
+    const int bytes = (int)a.in_row, steps = (bytes + 127) / 128;
+    // piece c of row r, so that eight rows' same pieces fall into different banks
+    auto place = [](int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); };
     for (int64_t t = blockIdx.x; t < (int64_t)mt * nt; t += gridDim.x) {
         const int col0 = (int)(t % nt) * cols;
         const Piece p = find_piece(a, ends, each, (int)(t / nt), pieces);
-        const int g = p.group;
-        const Group grp = p.rows;
-        const int m0 = p.n * kGenM;
-        const int rows = min(kGenM, grp.rows - m0);
-        const uint8_t* in = a.in + (grp.row + m0) * a.in_row;
-        uint8_t* out = a.out + (grp.row + m0) * a.out_row;
-        const int width = min(cols, a.width - col0);
-        float acc[2][4] = {};
-        for (int k0 = 0; k0 < a.K; k0 += kGenK) {
-            for (int i = threadIdx.x; i < kGenM * kGenK; i += kGenThreads) {
-                const int r = i / kGenK, k = k0 + i % kGenK;
-                xs[r][i % kGenK] = r < rows && k < a.K ? load_in(a, in + r * a.in_row, k) : 0.0f;
+        const int m0 = p.n * kGenRows, rows = min(kGenRows, p.rows.rows - m0);
+        const uint8_t* in = a.in + (p.rows.row + m0) * a.in_row;
+        uint8_t* out = a.out + (p.rows.row + m0) * a.out_row;
+        const uint8_t* weight = a.weight + (int64_t)p.group * a.N * a.w_row;
+        // this thread's pieces: rows threadIdx.x / 8 and 32 on.  With SwiGLU a wavefront's 16 weight
+        // rows are 8 columns' gate rows and their up rows.
+        const int c = threadIdx.x % 8;
+        const uint8_t *xr[2], *wr[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = threadIdx.x / 8 + 32 * i;
+            xr[i] = r < rows ? in + r * a.in_row : nullptr;
+            const int col = a.swiglu ? col0 + r / 16 * 8 + r % 8 : col0 + r;
+            wr[i] = col < a.width ? weight + (int64_t)(a.swiglu ? col + r / 8 % 2 * a.width : col) * a.w_row : nullptr;
+        }
+        u32x4 xv[2], wv[2];
+        auto load = [&](int s) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                xv[i] = wv[i] = u32x4{0, 0, 0, 0};
+                if (xr[i]) xv[i] = row_piece<T>(xr[i], s * 128 + c * 16, bytes);
+                if (wr[i]) wv[i] = row_piece<T>(wr[i], s * 128 + c * 16, bytes);
             }
-            for (int i = threadIdx.x; i < kGenN * kGenK; i += kGenThreads) {
-                // with SwiGLU weight rows come in pairs: tile row 2c is column c's gate, 2c + 1 its up
-                const int r = i / kGenK, k = k0 + i % kGenK;
-                const int c = a.swiglu ? r / 2 : r;
-                const int64_t wr = (int64_t)g * a.N + col0 + c + (a.swiglu && r % 2 ? a.width : 0);
-                ws[r][i % kGenK] = c < width && k < a.K ? load_weight(a, wr, k) : 0.0f;
+        };
+        f32x4 acc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = f32x4{0, 0, 0, 0};
+        load(0);
+        for (int s = 0; s < steps; ++s) {
+            __syncthreads();                                 // the step before has been read
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = threadIdx.x / 8 + 32 * i;
+                *(u32x4*)(xs + place(r, c)) = xv[i];
+                *(u32x4*)(ws + place(r, c)) = wv[i];
             }
             __syncthreads();
-#pragma unroll 8
-            for (int k = 0; k < kGenK; ++k)
+            if (s + 1 < steps) load(s + 1);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+            for (int k = 0; k < 2; ++k) {
+                const u32x4 w = *(const u32x4*)(ws + place(wave * 16 + l16, k * 4 + g));
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[tm + i][k], ws[tn + j][k], acc[i][j]);
-            __syncthreads();
+                for (int i = 0; i < 4; ++i) acc[i] = multiply16<KIND>(w, *(const u32x4*)(xs + place(i * 16 + l16, k * 4 + g)), acc[i]);
+            }
         }
+        // lane (l16, g): columns 4g .. 4g + 3 of row l16; with SwiGLU lanes g >= 2 hold the ups
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i) {
+            f32x4 v = acc[i];
+            int at = wave * 16 + 4 * g;
+            bool on = true;
+            if (a.swiglu) {
+                at = wave * 8 + 4 * g;
+                on = g < 2;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (a.swiglu) {
-                    if (j % 2 == 0) res[tm + i][(tn + j) / 2] = silu_mul(acc[i][j], acc[i][j + 1]);
-                } else {
-                    res[tm + i][tn + j] = acc[i][j];
-                }
+                for (int e = 0; e < 4; ++e) v[e] = silu_mul(v[e], __shfl_xor(acc[i][e], 32));
             }
-        __syncthreads();
-        if (a.out_dtype != A2AV_MX8) {
-            for (int i = threadIdx.x; i < kGenM * kGenN; i += kGenThreads) {
-                const int r = i / kGenN, c = i % kGenN;
-                if (r >= rows || c >= width) continue;
-                uint8_t* p = out + r * a.out_row;
-                if (a.out_dtype == A2AV_F32) ((float*)p)[col0 + c] = res[r][c];
-                else ((u16*)p)[col0 + c] = (u16)f32_to_bf16(res[r][c]);
+            const int row = i * 16 + l16;
+            uint8_t* to = out + row * a.out_row;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int col = col0 + at + e;
+                if (!on || row >= rows || col >= a.width) continue;
+                if constexpr (KIND == kF32) ((float*)to)[col] = v[e];
+                else ((u16*)to)[col] = (u16)f32_to_bf16(v[e]);
             }
-        } else {
-            // width is a multiple of 32, so is every tile's: one thread a scale
-            const int groups = width / kMxGroup;
-            for (int i = threadIdx.x; i < rows * groups; i += kGenThreads) {
-                const int r = i / groups, c0 = i % groups * kMxGroup;
-                uint32_t m = 0;
-                for (int c = 0; c < kMxGroup; ++c) m = max(m, abs_bits(res[r][c0 + c]));
-                const uint32_t sb = mx_scale_byte(m);
-                const float f = mx_inverse(sb);
-                uint8_t* p = out + r * a.out_row;
-                for (int c = 0; c < kMxGroup; c += 4)
-                    *(uint32_t*)(p + col0 + c0 + c) = mx8_pack(res[r][c0 + c] * f, res[r][c0 + c + 1] * f,
-                                                               res[r][c0 + c + 2] * f, res[r][c0 + c + 3] * f, sb == 255u);
-                p[a.width + (col0 + c0) / kMxGroup] = (uint8_t)sb;
-            }
-            const int used = a.width + a.width / kMxGroup, pad = (int)a.out_row - used;
-            if (col0 + width == a.width)
-                for (int i = threadIdx.x; i < rows * pad; i += kGenThreads) out[i / pad * a.out_row + used + i % pad] = 0;
         }
-        __syncthreads();
     }
+#endif
 }
 
 bool make_args(const a2av_matmul_t* c, ExpertArgs* a) {
@@ -136,6 +143,7 @@ bool make_args(const a2av_matmul_t* c, ExpertArgs* a) {
     if (c->activation == A2AV_ACT_SWIGLU && c->n % 2 != 0) return false;
     const int32_t width = c->activation == A2AV_ACT_SWIGLU ? c->n / 2 : c->n;
     if (o == A2AV_MX8 && width % kMxGroup != 0) return false;
+    if (c->n * (w == A2AV_MX4 ? c->k / 2 : w == A2AV_MX8 ? (int64_t)c->k : a2av_row_bytes(w, c->k)) > INT32_MAX) return false;
     a->cap = c->capacity_rows;
     a->in_row = a2av_row_bytes(i, c->k);
     a->w_row = w == A2AV_MX4 ? c->k / 2 : w == A2AV_MX8 ? c->k : a2av_row_bytes(w, c->k);
@@ -158,11 +166,12 @@ size_t alignment_of(int32_t dtype) { return dtype == A2AV_F32 ? 4 : dtype == A2A
 }  // namespace
 
 hipError_t launch_experts_general(const ExpertArgs& a, int num_cu, hipStream_t st) {
-    const int64_t mt = std::min<int64_t>((a.R * a.cap + kGenM - 1) / kGenM + a.G, INT32_MAX);
-    const int cols = a.swiglu ? kGenN / 2 : kGenN;
+    const int64_t mt = std::min<int64_t>(a.R * a.cap / kGenRows + a.G, INT32_MAX);
+    const int cols = a.swiglu ? kGenRows / 2 : kGenRows;
     const int64_t tiles = mt * ((a.width + cols - 1) / cols);
-    const unsigned grid = (unsigned)std::min<int64_t>(tiles, (int64_t)num_cu * 4);
-    hipLaunchKernelGGL(expert_general_kernel, dim3(grid), dim3(kGenThreads), 0, st, a);
+    const dim3 grid((unsigned)std::min<int64_t>(tiles, (int64_t)num_cu * 4));
+    if (kind_of(a) == kF32) hipLaunchKernelGGL((expert_general_kernel<kF32>), grid, dim3(kGenThreads), 0, st, a);
+    else hipLaunchKernelGGL((expert_general_kernel<kBf16>), grid, dim3(kGenThreads), 0, st, a);
     return hipGetLastError();
 }
 
@@ -201,7 +210,7 @@ extern "C" int a2av_expert_matmul(const a2av_matmul_t* cfg, const void* in, cons
     a.status = status;
     hipStream_t st = static_cast<hipStream_t>(stream);
     hipError_t e;
-    if (experts_mfma_takes(a)) {
+    if (experts_whole_pieces(a)) {
         a.few = few_rows(a);
         a.tile_least = few_rows_all(a) ? cus / 2 : 0;
         e = launch_experts_few(a, cus, st);

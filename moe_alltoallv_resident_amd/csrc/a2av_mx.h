@@ -49,11 +49,6 @@ __device__ inline uint32_t mx_scale_byte(uint32_t a) {
 // 1 / 2^(byte - 127); byte <= 247 for every finite group, so it is a normal number.
 __device__ inline float mx_inverse(uint32_t byte) { return __uint_as_float((254u - (byte > 253u ? 253u : byte)) << 23); }
 
-// 2^(byte - 127): byte 0 is 2^-127, 255 is NaN.
-__device__ inline float mx_scale(uint32_t byte) {
-    return byte == 0 ? __uint_as_float(0x00400000u) : byte == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23);
-}
-
 // Four floats (already divided by their scale) as four e4m3 bytes.  A group whose scale is
 // NaN holds 0x7F (NaN) everywhere.
 __device__ inline uint32_t mx8_pack(float a, float b, float c, float d, bool bad) {
@@ -64,21 +59,6 @@ __device__ inline uint32_t mx8_pack(float a, float b, float c, float d, bool bad
 #else
     return 0;
 #endif
-}
-
-__device__ inline float e4m3_to_f32(uint32_t byte) {
-#ifdef A2AV_DEVICE_CODE
-    return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0);
-#else
-    return 0.0f;
-#endif
-}
-
-// E2M1: sign, two exponent bits, one fraction bit; 0 and 0.5 below 1.
-__device__ inline float e2m1_to_f32(uint32_t nibble) {
-    const uint32_t e = (nibble >> 1) & 3u, f = nibble & 1u;
-    const float m = e ? __uint_as_float(((126u + e) << 23) | (f << 22)) : 0.5f * (float)f;
-    return nibble & 8u ? -m : m;
 }
 
 }  // namespace a2av

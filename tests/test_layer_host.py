@@ -69,6 +69,7 @@ FPW = dict(weight_dtype=a2av.MX4, scales=P(5))
     dict(off=None), dict(weight=None), dict(status=None), dict(inp=None), dict(out=None),
     dict(off=P(1, 2)), dict(status=P(4, 1)), dict(inp=P(0, 1)), dict(out=P(3, 1)), dict(weight=P(2, 1)),
     dict(MXW, inp=P(0, 8)), dict(MXW, weight=P(2, 8)), dict(FPW, weight=P(2, 4)), dict(MXW, out=P(3, 8), out_dtype=a2av.MX8),
+    dict(k=1 << 15, n=1 << 15), dict(FPW, k=1 << 16, n=1 << 16),      # an expert's weight of 2 GiB
     dict(out=P(0)), dict(out=P(0, 1024)), dict(out=P(2)), dict(out=P(1, -8)), dict(FPW, out=P(5)),
 ])
 def test_matmul_refuses(bad):
