@@ -192,6 +192,18 @@ def test_more_groups_than_threads():
     Case(np.zeros((4, 8), np.int64), 64, 64, KINDS[1], False).run().check()
 
 
+@pytest.mark.parametrize("kind,k", [(KINDS[1], 64), (KINDS[4], 128), (KINDS[0], 33), (KINDS[1], 33)],
+                         ids=["bf16", "mx8", "f32-odd", "bf16-odd"])
+def test_many_groups_with_many_rows(kind, k):
+    """More groups than the list of row tiles has entries, some of several tiles."""
+    rng = np.random.default_rng(4)
+    counts = rng.integers(0, 2, (75, 16))
+    for at in (3, 599, 600, 607, 1100):
+        counts.flat[at] = 700 + at % 7
+    counts[74, 15] = 300
+    Case(counts, k, 2112, kind, False).run().check()
+
+
 @kinds
 def test_infinities_and_nan_stay_in_their_row(kind):
     """A NaN in a row or an infinity in it reaches that row's outputs and no other's."""
@@ -337,6 +349,53 @@ def test_8_bit_rows_through_the_exchange(path, R, T, epr, top_k, cap):
             a2av.a2av_expert_apply(m.handle, m.recv, m.recv, a2av.EXPERT_IDENTITY)
         for s in (m, b, o):
             s.close()
+
+
+def test_8_bit_rows_through_the_bare_collective():
+    R, T, H = 4, 40, 96
+    row = a2av.a2av_row_bytes(MX8, H)
+    g = torch.Generator().manual_seed(6)
+    send = torch.randint(0, 256, (R, T, row), generator=g, dtype=torch.uint8).cuda()
+    counts = torch.tensor([[10, 0, 20, 5], [0, 0, 0, 40], [1, 2, 3, 4], [0, 0, 0, 0]], dtype=torch.int32).cuda()
+    out = []
+    for dtype, hidden in ((MX8, H), (BF16, row // 2)):
+        cfg = a2av.make_config(R, T, hidden, dtype, 1, 1)
+        recv = torch.zeros((R, R * T, row), dtype=torch.uint8, device="cuda")
+        again = torch.zeros_like(recv)
+        rc, st = torch.zeros((R, R), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        h = a2av.a2av_create(cfg)
+        a2av.a2av_alltoallv(h, send, counts, recv, rc, None, st)
+        a2av.a2av_alltoallv_noalloc(cfg, send, counts, again, rc, None, st)
+        torch.cuda.synchronize()
+        a2av.a2av_destroy(h)
+        assert int(st.item()) == 0 and torch.equal(recv, again)
+        out.append(recv)
+    assert torch.equal(out[0], out[1]) and out[0].any()
+
+
+def test_group_starts_of_the_handle():
+    """The handle's own table is what the copy gives, before and after a dispatch, and only
+    expert-major handles have one."""
+    s = a2av.Session(2, 8, 64, BF16, 3, 2, recv_layout=a2av.LAYOUT_EXPERT_MAJOR)
+    x = rows_of((2, 8, 64), BF16, 0)
+    ids = torch.randint(0, 6, (2, 8, 2), generator=torch.Generator().manual_seed(1), dtype=torch.int32).cuda()
+    w = rows_of((6, 32, 64), BF16, 1)
+    out = torch.full((2, s.cap, 32), 77, dtype=torch.bfloat16, device="cuda")
+    s.expert_matmul(s.recv, w, out)                          # nothing dispatched yet: every group is empty
+    torch.cuda.synchronize()
+    assert (out == 77).all()
+    s.dispatch(x, ids)
+    s.expert_matmul(s.recv, w, out)
+    want = torch.full_like(out, 77)
+    a2av.expert_matmul(s.recv, s.recv_expert_offsets(), w, want, s.status)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and not (out == 77).all() and int(s.status.item()) == 0
+    assert int(s.recv_expert_offsets()[:, -1].sum()) == 2 * 8 * 2
+    t = a2av.Session(2, 8, 64, BF16, 3, 2)
+    assert not a2av.a2av_recv_expert_offsets(t.handle)
+    with pytest.raises(ValueError):
+        t.expert_matmul(t.recv, w, out)
+    s.close(), t.close()
 
 
 @pytest.mark.parametrize("weight", [MX8, MX4], ids=["mx8", "mx4"])
