@@ -227,30 +227,33 @@ __device__ inline f32x16 multiply32(u32x4 w0, u32x4 w1, int ws, u32x4 x0, u32x4 
     }
 }
 
+// The LDS address of a shared array: what the loads below take.
+__device__ inline uint32_t lds_address(const void* shared) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)shared);
+}
+
 // 16 bytes a lane, from each lane's offset straight to 1024 neighbouring bytes of LDS.  Written as
 // an instruction without outputs: with the builtin the compiler waits for every such load before
 // the next read of any LDS, so that nothing could be loaded while a step is multiplied.  Whoever
 // reads the bytes calls wait_for_loads first, and a barrier where other wavefronts loaded them.
-__device__ inline void load_to_lds(u32x4 buf, const void* lds, uint32_t voffset, uint32_t soffset) {
-    const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds;
+__device__ inline void load_to_lds(u32x4 buf, uint32_t lds, uint32_t voffset, uint32_t soffset) {
     u32x4 b;                                             // scalar registers, whatever the compiler thinks of it
 #pragma unroll
     for (int i = 0; i < 4; ++i) b[i] = __builtin_amdgcn_readfirstlane(buf[i]);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
-                 : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(voffset), "s"(b), "s"(__builtin_amdgcn_readfirstlane(soffset))
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voffset), "s"(b), "s"(__builtin_amdgcn_readfirstlane(soffset))
                  : "memory");
 }
 
 // The same with 4 bytes a lane and 256 of LDS.
-__device__ inline void load_word_to_lds(u32x4 buf, const void* lds, uint32_t voffset, uint32_t soffset) {
-    const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds;
+__device__ inline void load_word_to_lds(u32x4 buf, uint32_t lds, uint32_t voffset, uint32_t soffset) {
     u32x4 b;
 #pragma unroll
     for (int i = 0; i < 4; ++i) b[i] = __builtin_amdgcn_readfirstlane(buf[i]);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
                  :
-                 : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(voffset), "s"(b), "s"(__builtin_amdgcn_readfirstlane(soffset))
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voffset), "s"(b), "s"(__builtin_amdgcn_readfirstlane(soffset))
                  : "memory");
 }
 

@@ -239,6 +239,7 @@ __device__ __forceinline__ void run_stream(const ExpertArgs& a, const Job& t, ui
     const int steps = (a.K + R::kElems - 1) / R::kElems;
     const int x_bytes = KIND == kF32 ? a.K * 4 : KIND == kBf16 || KIND == kBf16Mx4 ? a.K * 2 : a.K;
     const int blocks = a.K / kMxGroup;
+    const uint32_t lds_at = lds_address(lds);
     uint8_t* scales = lds + kDepth * R::kStage;              // two times sixteen blocks' bytes of the weight and input rows
 
     const u32x4 xbuf = buffer_words(t.in, (uint32_t)(t.rows * a.in_row));
@@ -277,9 +278,9 @@ __device__ __forceinline__ void run_stream(const ExpertArgs& a, const Job& t, ui
     const bool x_wave = R::kXLoads % kWaves == 0 || (R::kXPer - 1) * kWaves + wave < R::kXLoads;   // makes all kXPer loads
     // Past the last stage everything reads zeros: the counts that the waits go by stay the same.
     auto load = [&](int s) __attribute__((always_inline)) {
-        uint8_t* st = lds + s % kDepth * R::kStage;
+        const uint32_t st = lds_at + s % kDepth * R::kStage;
         if (weight_scaled(KIND) && scale_wave && s * kBlocks % 16 == 0 && s < steps)
-            load_to_lds(sbuf, scales + (s * kBlocks / 16 % 2) * ((kStreamRows + 64) * 16) + wave * 1024, so, s * kBlocks);
+            load_to_lds(sbuf, lds_at + kDepth * R::kStage + (s * kBlocks / 16 % 2) * ((kStreamRows + 64) * 16) + wave * 1024, so, s * kBlocks);
         const bool in = s < steps, last = s == steps - 1;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
