@@ -223,11 +223,15 @@ struct Ring {
     static_assert(kResult <= kDepth * kStage, "results fit the ring");
 };
 
-// Place of 16-byte piece c of row r in LDS rows of ROW bytes: eight rows' same pieces, read by
-// eight neighbouring lanes, fall into different banks.
+// Place of 16-byte piece c of row r in LDS rows of ROW bytes: the same pieces of sixteen rows fall
+// into different banks.
+template <int ROW>
+__device__ inline int moved(int r) {
+    return ROW == 128 ? r & 7 : r & 15;
+}
 template <int ROW>
 __device__ inline int place_of(int r, int c) {
-    return r * ROW + ((c ^ (r & 7)) << 4);
+    return r * ROW + ((c ^ moved<ROW>(r)) << 4);
 }
 
 template <int KIND, int MT>
@@ -260,7 +264,7 @@ __device__ __forceinline__ void run_stream(const ExpertArgs& a, const Job& t, ui
     bool x_over[R::kXPer];
 #pragma unroll
     for (int i = 0; i < R::kXPer; ++i) {
-        const int r = (i * kWaves + wave) * (1024 / kXRow) + lane / kXPieces, c = ((lane % kXPieces) ^ (r & 7)) * 16;
+        const int r = (i * kWaves + wave) * (1024 / kXRow) + lane / kXPieces, c = ((lane % kXPieces) ^ moved<kXRow>(r)) * 16;
         xo[i] = (uint32_t)(r * a.in_row + c);                // rows past the last: past the buffer's end
         x_over[i] = c >= x_bytes - (steps - 1) * kXRow;
     }

@@ -49,21 +49,19 @@ struct Shared {
     uint32_t ahead[kWaves][kWave];   // what is loaded only to have it in the L2 goes here
 };
 
-// Where 16-byte piece c of row r stands in its LDS row: eight neighbouring rows' same pieces, read
-// by eight neighbouring lanes, fall into different banks.
+// Where 16-byte piece c of row r stands in its LDS row: the same pieces of any sixteen rows that
+// differ modulo 16 fall into different banks (with the pieces moved by the row modulo 8 instead, half
+// of the LDS cycles were conflicts).
+[[maybe_unused]] __host__ __device__ constexpr int moved(int step, int r) { return step == 128 ? r >> 1 & 7 : step == 64 ? r >> 2 & 3 : r >> 3 & 1; }
 template <int STEP>
 __device__ inline int place(int r, int c) {
-    if constexpr (STEP == 128) return r * 128 + ((c ^ (r & 7)) << 4);
-    else if constexpr (STEP == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-    else return r * 32 + (c << 4);
+    return r * STEP + ((c ^ moved(STEP, r)) << 4);
 }
 
 // The piece that belongs at place p of row r.
 template <int STEP>
 __device__ inline int piece_at(int r, int p) {
-    if constexpr (STEP == 128) return p ^ (r & 7);
-    else if constexpr (STEP == 64) return p ^ ((r >> 1) & 3);
-    else return p;
+    return p ^ moved(STEP, r);
 }
 
 // Row pieces of 32 for each of the two wavefronts along the rows: a tile has 64 * 4, 2 or 1 rows.
@@ -116,12 +114,12 @@ struct Loader {
         xbuf = buffer_words(t.in, (uint32_t)(t.rows * a.in_row));
         wbuf = buffer_words(t.weight, (uint32_t)(a.N * a.w_row));
         const int x_bytes = KIND == kF32 ? a.K * 4 : KIND == kBf16 || KIND == kBf16Mx4 ? a.K * 2 : a.K;
-        // row 8 n + lane / 8: its swizzle, and so its piece, is the same for every n
-        const int xc = piece_at<128>(lane / 8, lane % 8) * 16;
+        // load i has row 8 (4 i + wave) + lane / 8: its piece's move is the same for every i
+        const int xc = piece_at<128>(wave * 8 + lane / 8, lane % 8) * 16;
         x_over = xc >= x_bytes - (steps - 1) * kRowStep;
 #pragma unroll
         for (int i = 0; i < kXLoads; ++i) xo[i] = (uint32_t)(((i * kWaves + wave) * 8 + lane / 8) * a.in_row + xc);
-        const int wc = piece_at<kWStep>(lane / kWPieces, lane % kWPieces) * 16;
+        const int wc = piece_at<kWStep>(wave * kWRows + lane / kWPieces, lane % kWPieces) * 16;
         w_over = wc >= (int)a.w_row - (steps - 1) * kWStep;
 #pragma unroll
         for (int i = 0; i < kWLoads; ++i) {
@@ -236,8 +234,8 @@ __device__ __forceinline__ void run_tile(const ExpertArgs& a, const Tile& t, Sha
             const int r = wn * 128 + n * 32 + l32;
             if constexpr (KIND == kBf16Mx4) {
                 const float scale = __uint_as_float((uint32_t)sc[r * kQuad + k] << 23);
-                f.w[n][0] = widen_e2m1(*(const uint32_t*)(st.w + r * kWStep + k * 16 + h * 4), scale);
-                f.w[n][1] = widen_e2m1(*(const uint32_t*)(st.w + r * kWStep + k * 16 + 8 + h * 4), scale);
+                f.w[n][0] = widen_e2m1(*(const uint32_t*)(st.w + place<kWStep>(r, k) + h * 4), scale);
+                f.w[n][1] = widen_e2m1(*(const uint32_t*)(st.w + place<kWStep>(r, k) + 8 + h * 4), scale);
             } else if constexpr (KIND == kMx8Mx4) {
                 f.w[n][0] = *(const u32x4*)(st.w + place<kWStep>(r, k * 2 + h));
                 f.w[n][1] = u32x4{0, 0, 0, 0};
