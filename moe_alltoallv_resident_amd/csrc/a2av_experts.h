@@ -270,6 +270,24 @@ __device__ inline void block_barrier() {
     asm volatile("" : : : "memory");
 }
 
+// Sixteen scale bytes from p on, of which `valid` belong to the row (the others become zero: what
+// they scale is zero, but a NaN byte would make it NaN) and `readable` may be read.  For rows of
+// scales that are not whole words, which cannot be loaded straight to LDS.
+__device__ inline u32x4 scale_bytes(const uint8_t* p, int valid, int64_t readable) {
+    u32x4 v = {0, 0, 0, 0};
+    if (valid <= 0) return v;
+    if (readable >= 16) {
+        __builtin_memcpy(&v, p, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < valid) v[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) v[w] &= valid >= 4 * w + 4 ? ~0u : valid <= 4 * w ? 0u : (1u << (8 * (valid - 4 * w))) - 1u;
+    return v;
+}
+
 // Lanes of this wavefront hand each other values through LDS: what was written before it is read
 // after it (LDS instructions of a wavefront are carried out in order).
 __device__ inline void wave_sync() {
@@ -335,7 +353,6 @@ hipError_t launch_experts_general(const ExpertArgs& a, int num_cu, hipStream_t s
 // Groups of 1 .. a.few rows; of more as well, in pieces of a.few, where they would make tiles for
 // fewer than half of the CUs (a.tile_least).
 int few_rows(const ExpertArgs& a);
-bool few_rows_all(const ExpertArgs& a);
 hipError_t launch_experts_few(const ExpertArgs& a, int num_cu, hipStream_t st);
 // Groups of more rows.
 hipError_t launch_experts_tile(const ExpertArgs& a, int num_cu, hipStream_t st);

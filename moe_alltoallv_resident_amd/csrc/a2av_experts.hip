@@ -212,13 +212,13 @@ extern "C" int a2av_expert_matmul(const a2av_matmul_t* cfg, const void* in, cons
     hipError_t e;
     if (experts_whole_pieces(a)) {
         a.few = few_rows(a);
-        a.tile_least = few_rows_all(a) ? cus / 2 : 0;
+        a.tile_least = std::max(cus / 2, 1);
         e = launch_experts_few(a, cus, st);
         // a group of more rows needs a capacity of more, and a tile's worth of groups needs rows enough
         // (a group of r > few rows makes at most r / few row tiles)
         const int64_t most = a.cap > a.few ? a.R * a.cap / a.few : 0;
         const int cols = a.swiglu ? kTileRows / 2 : kTileRows;
-        if (e == hipSuccess && most * ((a.width + cols - 1) / cols) >= std::max(a.tile_least, 1)) e = launch_experts_tile(a, cus, st);
+        if (e == hipSuccess && most * ((a.width + cols - 1) / cols) >= a.tile_least) e = launch_experts_tile(a, cus, st);
     } else {
         e = launch_experts_general(a, cus, st);
     }

@@ -11,6 +11,8 @@
 // registers, so that as many CUs as possible read; the parts are added through LDS.
 #include "a2av_experts.h"
 
+#include <type_traits>
+
 namespace a2av {
 namespace {
 
@@ -234,7 +236,9 @@ __device__ inline int place_of(int r, int c) {
     return r * ROW + ((c ^ moved<ROW>(r)) << 4);
 }
 
-template <int KIND, int MT>
+// WHOLE: rows of scales are whole words; else (a width that is no multiple of 128) they go through
+// registers.
+template <int KIND, int MT, bool WHOLE>
 __device__ __forceinline__ void run_stream(const ExpertArgs& a, const Job& t, uint8_t* lds) {
     using R = Ring<KIND, MT>;
     constexpr int kXRow = R::kXRow, kXPieces = kXRow / 16, kDepth = R::kDepth;
@@ -283,8 +287,15 @@ __device__ __forceinline__ void run_stream(const ExpertArgs& a, const Job& t, ui
     // Past the last stage everything reads zeros: the counts that the waits go by stay the same.
     auto load = [&](int s) __attribute__((always_inline)) {
         const uint32_t st = lds_at + s % kDepth * R::kStage;
-        if (weight_scaled(KIND) && scale_wave && s * kBlocks % 16 == 0 && s < steps)
-            load_to_lds(sbuf, lds_at + kDepth * R::kStage + (s * kBlocks / 16 % 2) * ((kStreamRows + 64) * 16) + wave * 1024, so, s * kBlocks);
+        if (weight_scaled(KIND) && scale_wave && s * kBlocks % 16 == 0 && s < steps) {
+            if (WHOLE)
+                load_to_lds(sbuf, lds_at + kDepth * R::kStage + (s * kBlocks / 16 % 2) * ((kStreamRows + 64) * 16) + wave * 1024, so, s * kBlocks);
+            else
+                *(u32x4*)(scales + (s * kBlocks / 16 % 2) * ((kStreamRows + 64) * 16) + wave * 1024 + lane * 16) =
+                    so == kOutside ? u32x4{0, 0, 0, 0}
+                                   : scale_bytes((wave < 2 ? t.scales : t.in) + so + s * kBlocks, blocks - s * kBlocks,
+                                                 wave < 2 ? (int64_t)a.N * blocks - so - s * kBlocks : a.in_row - a.K - s * kBlocks);
+        }
         const bool in = s < steps, last = s == steps - 1;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -320,7 +331,7 @@ __device__ __forceinline__ void run_stream(const ExpertArgs& a, const Job& t, ui
         } else if constexpr (KIND == kBf16Mx4) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                if (u && s * kBlocks + 4 >= blocks) break;   // the row ends after 128 elements: no scales here
+                if (u && s * kBlocks + 4 >= blocks) break;   // the row has ended: no scales here
                 // a lane's 16 bytes are 32 elements, a scale's
                 const float f = __uint_as_float((uint32_t)sc[(wave * 16 + l16) * 16 + u * 4 + g] << 23);
 #pragma unroll
@@ -404,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2 * kBlocksPerCu) expert_few_kernel(
     int n = __builtin_amdgcn_readfirstlane(all ? n4.v[1] : n4.v[0]);
     if (n == 0) return;
     const bool direct = __builtin_amdgcn_readfirstlane(n4.v[3]) > 0 &&
-                        (a.few == kDirectRows || (int64_t)n * nt_stream < gridDim.x / kBlocksPerCu);
+                        (int64_t)n * nt_stream < gridDim.x / kBlocksPerCu;
     if (direct) {
         // Not a stream tile for every CU: groups of up to 16 rows go by smaller pieces.  Every row's
         // length is cut into as many parts as a block has wavefronts.
@@ -419,17 +430,20 @@ __global__ void __launch_bounds__(kThreads, 2 * kBlocksPerCu) expert_few_kernel(
         const int nt = (a.width + cols - 1) / cols;
         for (int64_t t = blockIdx.x; t < (int64_t)n * nt; t += gridDim.x)
             run_direct<KIND>(a, job_at((int)(t / nt), (int)(t % nt) * cols), parts, (f32x4*)lds);
-        if (a.few == kDirectRows) return;
         lo = kDirectRows;
         hi = limit;
     }
     n = list();
-    for (int64_t t = blockIdx.x; t < (int64_t)n * nt_stream; t += gridDim.x) {
-        const Job job = job_at((int)(t / nt_stream), (int)(t % nt_stream) * cols_stream);
-        if (job.rows <= 16) run_stream<KIND, 1>(a, job, lds);
-        else if (KIND == kBf16Mx4 || job.rows <= 32) run_stream<KIND, 2>(a, job, lds);
-        else if constexpr (KIND != kBf16Mx4) run_stream<KIND, 4>(a, job, lds);
-    }
+    auto stream = [&](auto whole) __attribute__((always_inline)) {
+        for (int64_t t = blockIdx.x; t < (int64_t)n * nt_stream; t += gridDim.x) {
+            const Job job = job_at((int)(t / nt_stream), (int)(t % nt_stream) * cols_stream);
+            if (job.rows <= 16) run_stream<KIND, 1, whole.value>(a, job, lds);
+            else if (KIND == kBf16Mx4 || job.rows <= 32) run_stream<KIND, 2, whole.value>(a, job, lds);
+            else if constexpr (KIND != kBf16Mx4) run_stream<KIND, 4, whole.value>(a, job, lds);
+        }
+    };
+    if (!weight_scaled(KIND) || (a.K / kMxGroup % 4 == 0 && (uintptr_t)a.scales % 4 == 0)) stream(std::true_type());
+    else if constexpr (weight_scaled(KIND)) stream(std::false_type());
 #endif
 }
 
@@ -442,14 +456,8 @@ hipError_t launch(const ExpertArgs& a, int num_cu, hipStream_t st) {
 }  // namespace
 
 // The stream takes up to 64 input rows, 32 of bfloat16 with 4-bit weights (their 256 elements of a
-// stage are 512 bytes); its scales are loaded in whole words.
-int few_rows(const ExpertArgs& a) {
-    const Kind k = kind_of(a);
-    if (weight_scaled(k) && (a.K % 128 != 0 || (uintptr_t)a.scales % 4 != 0)) return kDirectRows;
-    return k == kBf16Mx4 ? 32 : 64;
-}
-
-bool few_rows_all(const ExpertArgs& a) { return a.few > kDirectRows; }
+// stage are 512 bytes).
+int few_rows(const ExpertArgs& a) { return kind_of(a) == kBf16Mx4 ? 32 : 64; }
 
 hipError_t launch_experts_few(const ExpertArgs& a, int num_cu, hipStream_t st) {
     switch (kind_of(a)) {

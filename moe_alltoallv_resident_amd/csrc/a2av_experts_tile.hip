@@ -91,7 +91,7 @@ struct Loader {
     u32x4 xbuf, wbuf, sbuf;
     uint32_t xo[kXLoads], wo[kWLoads], wso, xso, xrow;
     bool x_over, w_over;     // the lane's pieces are past the row's end in the last step
-    const uint8_t *wsp, *xsp;   // scales that are read byte by byte
+    const uint8_t *wsp, *xsp;   // for scales that go through registers
 
     // weight row of tile row r: with SwiGLU 32 gate rows and the 32 up rows of the same columns in turn
     static __device__ int weight_row(const ExpertArgs& a, const Tile& t, int r) {
@@ -160,8 +160,8 @@ struct Loader {
         if (n < kWLoads) weights(s, n);
         else rows(s, n - kWLoads);
     }
-    // Scale bytes, sixteen blocks at a time.  Rows of scales that are not whole words (a width that
-    // is no multiple of 128) are read byte by byte.
+    // Scale bytes, sixteen blocks at a time; rows of scales that are not whole words (a width that is
+    // no multiple of 128) go through registers.
     __device__ __forceinline__ void scales(const ExpertArgs& a, int quad) {
         if (!weight_scaled(KIND) || quad * kQuad >= blocks) return;
         if (blocks % 4 == 0 && (uintptr_t)a.scales % 4 == 0) {
@@ -169,17 +169,14 @@ struct Loader {
             load_to_lds(sbuf, to, wso, quad * kQuad);
             if (rows_scaled(KIND)) load_to_lds(xbuf, to + kTileN * kQuad, xso, quad * kQuad);
         } else {
-            bytes(sh.scales[quad & 1].of[wave * kWave], wsp, wso, quad);
-            if (rows_scaled(KIND)) bytes(sh.scales[quad & 1].of[kTileN + wave * kWave], xsp, xso, quad);
-        }
-    }
-    __device__ __forceinline__ void bytes(uint8_t* to, const uint8_t* from, uint32_t at, int quad) {
-#pragma unroll 1
-        for (int w = 0; w < kQuad; w += 4) {
-            uint32_t v = 0;
-            for (int i = 0; i < 4; ++i)
-                if (at != kOutside && quad * kQuad + w + i < blocks) v |= (uint32_t)from[at + quad * kQuad + w + i] << (8 * i);
-            *(uint32_t*)(to + lane * kQuad + w) = v;
+            const int valid = blocks - quad * kQuad;
+            u32x4 w = {0, 0, 0, 0}, x = w;
+            if (wso != kOutside)
+                w = scale_bytes(wsp + wso + quad * kQuad, valid, (int64_t)a.N * blocks - wso - quad * kQuad);
+            if (rows_scaled(KIND) && xso != kOutside)
+                x = scale_bytes(xsp + xso + quad * kQuad, valid, a.in_row - a.K - quad * kQuad);
+            *(u32x4*)sh.scales[quad & 1].of[wave * kWave + lane] = w;
+            if (rows_scaled(KIND)) *(u32x4*)sh.scales[quad & 1].of[kTileN + wave * kWave + lane] = x;
         }
     }
 };
