@@ -16,30 +16,46 @@ constexpr int32_t kMaxDim = 1 << 20;
 // ---- rows that are not whole 16-byte pieces ------------------------------------------
 // float32 and bfloat16 rows of any length and address.  64 input rows by 64 weight rows a tile,
 // 128 bytes of each a step: through registers into LDS, 16 bytes at a time wherever the row's
-// elements lie (the memory takes such loads at any address), the last ones of a row element by
-// element.  The next step's loads run while a step is multiplied.
-
+// elements lie (the memory takes such loads at any address).  What is left after a row's whole steps
+// comes first.  The next two steps' loads run while a step is multiplied; 3, 4 and 6 in flight were no
+// faster (8,192 bfloat16 rows x 4097 -> 2048 over 128 experts 0.84, 0.85, 0.84 and 0.87 ms, the
+// whole-piece kernels 0.45 ms at 4096).
+// With up to 16 rows a quarter of the products is made: 11 float32 rows x 1214 -> 104 take 21 us, all
+// four 34.
 [[maybe_unused]] constexpr int kGenThreads = 256;
 [[maybe_unused]] constexpr int kGenRows = 64;             // input rows and weight rows of a tile
+[[maybe_unused]] constexpr int kGenDepth = 2;             // steps whose loads are on their way
 
 #ifdef A2AV_DEVICE_CODE
-// The 16 bytes at `at` of a row of `bytes` bytes, zeros past its end.
+// The 16 bytes at `at` of a row of `bytes` bytes, zeros past its end: there the row's last 16 bytes,
+// moved down.
 template <typename T>
 __device__ inline u32x4 row_piece(const uint8_t* row, int at, int bytes) {
     u32x4 v = {0, 0, 0, 0};
-    if (at + 16 <= bytes) {
-        __builtin_memcpy(&v, row + at, 16);
-    } else {
+    if (at >= bytes) return v;
+    if (bytes >= 16) {
+        const int over = max(at + 16 - bytes, 0);
+        uint64_t lo, hi;
+        __builtin_memcpy(&lo, row + at - over, 8);
+        __builtin_memcpy(&hi, row + at - over + 8, 8);
+        const int by = 8 * (over % 8);
+        if (over >= 8) lo = hi, hi = 0;
+        if (by) lo = lo >> by | hi << (64 - by), hi >>= by;
+        v = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+    } else if (at == 0) {
+#pragma unroll 1
+        for (int e = 0; e < bytes; e += sizeof(T)) {
+            const uint32_t t = (uint32_t) * (const T*)(row + e) << (8 * (e % 4));
 #pragma unroll
-        for (int e = 0; e < 16; e += sizeof(T))
-            if (at + e < bytes) v[e / 4] |= (uint32_t) * (const T*)(row + at + e) << (8 * (e % 4));
+            for (int w = 0; w < 4; ++w) v[w] |= e / 4 == w ? t : 0;
+        }
     }
     return v;
 }
 #endif
 
 template <int KIND>
-__global__ void __launch_bounds__(kGenThreads) expert_general_kernel(ExpertArgs a) {
+__global__ void __launch_bounds__(kGenThreads, 4) expert_general_kernel(ExpertArgs a) {
 #ifdef A2AV_DEVICE_CODE
     using T = typename std::conditional<KIND == kF32, uint32_t, u16>::type;   // an element's bits
     __shared__ int ends[kEntries];
@@ -51,7 +67,7 @@ __global__ void __launch_bounds__(kGenThreads) expert_general_kernel(ExpertArgs 
     const int cols = a.swiglu ? kGenRows / 2 : kGenRows;     // output columns of a tile
     const int nt = (a.width + cols - 1) / cols;
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, l16 = lane % 16, g = lane / 16;
-    const int bytes = (int)a.in_row, steps = (bytes + 127) / 128;
+    const int bytes = (int)a.in_row, whole = bytes / 128;
     // piece c of row r, so that eight rows' same pieces fall into different banks
     auto place = [](int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); };
     for (int64_t t = blockIdx.x; t < (int64_t)mt * nt; t += gridDim.x) {
@@ -64,44 +80,69 @@ __global__ void __launch_bounds__(kGenThreads) expert_general_kernel(ExpertArgs 
         // this thread's pieces: rows threadIdx.x / 8 and 32 on.  With SwiGLU a wavefront's 16 weight
         // rows are 8 columns' gate rows and their up rows.
         const int c = threadIdx.x % 8;
-        const uint8_t *xr[2], *wr[2];
+        const uint8_t *xr[2], *wr[2];                        // past the last: the first, whose results are not written
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = threadIdx.x / 8 + 32 * i;
-            xr[i] = r < rows ? in + r * a.in_row : nullptr;
+            xr[i] = in + (r < rows ? r : 0) * a.in_row;
             const int col = a.swiglu ? col0 + r / 16 * 8 + r % 8 : col0 + r;
-            wr[i] = col < a.width ? weight + (int64_t)(a.swiglu ? col + r / 8 % 2 * a.width : col) * a.w_row : nullptr;
+            wr[i] = weight + (int64_t)(col >= a.width ? 0 : a.swiglu ? col + r / 8 % 2 * a.width : col) * a.w_row;
         }
-        u32x4 xv[2], wv[2];
-        auto load = [&](int s) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                xv[i] = wv[i] = u32x4{0, 0, 0, 0};
-                if (xr[i]) xv[i] = row_piece<T>(xr[i], s * 128 + c * 16, bytes);
-                if (wr[i]) wv[i] = row_piece<T>(wr[i], s * 128 + c * 16, bytes);
-            }
-        };
         f32x4 acc[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i] = f32x4{0, 0, 0, 0};
-        load(0);
-        for (int s = 0; s < steps; ++s) {
-            __syncthreads();                                 // the step before has been read
+        auto multiply = [&](const u32x4* xv, const u32x4* wv) __attribute__((always_inline)) {
+            block_barrier();                                 // the step before has been read
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = threadIdx.x / 8 + 32 * i;
                 *(u32x4*)(xs + place(r, c)) = xv[i];
                 *(u32x4*)(ws + place(r, c)) = wv[i];
             }
-            __syncthreads();
-            if (s + 1 < steps) load(s + 1);
+            block_barrier();
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const u32x4 w = *(const u32x4*)(ws + place(wave * 16 + l16, k * 4 + g));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[i] = multiply16<KIND>(w, *(const u32x4*)(xs + place(i * 16 + l16, k * 4 + g)), acc[i]);
+                for (int i = 0; i < 4; ++i) {
+                    if (i == 1 && rows <= 16) break;         // the other rows' results are not written
+                    acc[i] = multiply16<KIND>(w, *(const u32x4*)(xs + place(i * 16 + l16, k * 4 + g)), acc[i]);
+                }
             }
+        };
+        u32x4 xv[kGenDepth][2], wv[kGenDepth][2];
+        // Past the last whole step the last one again: no condition, so that the waits for a step's
+        // loads leave the later steps' loads on their way.
+        auto load = [&](int s, int slot) __attribute__((always_inline)) {
+            const int at = min(s, whole - 1) * 128 + c * 16;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                __builtin_memcpy(&xv[slot][i], xr[i] + at, 16);
+                __builtin_memcpy(&wv[slot][i], wr[i] + at, 16);
+            }
+        };
+        u32x4 xt[2], wt[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {                        // what is left of the rows after the whole steps
+            xt[i] = row_piece<T>(xr[i], whole * 128 + c * 16, bytes);
+            wt[i] = row_piece<T>(wr[i], whole * 128 + c * 16, bytes);
         }
+        if (whole > 0) {
+#pragma unroll
+            for (int j = 0; j < kGenDepth; ++j) load(j, j);
+        }
+        if (whole * 128 < bytes) multiply(xt, wt);
+#pragma unroll 1
+        for (int s = 0; s < whole; s += kGenDepth)
+#pragma unroll
+            for (int j = 0; j < kGenDepth; ++j) {
+                if (s + j >= whole) {                        // zeros: no way out of the middle of the loop
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) xv[j][i] = wv[j][i] = u32x4{0, 0, 0, 0};
+                }
+                multiply(xv[j], wv[j]);
+                load(s + j + kGenDepth, j);
+            }
         // lane (l16, g): columns 4g .. 4g + 3 of row l16; with SwiGLU lanes g >= 2 hold the ups
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
