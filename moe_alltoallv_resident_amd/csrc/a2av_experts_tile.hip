@@ -12,6 +12,10 @@
 // Matrix instructions: 32x32x16 (bfloat16), 32x32x2 (float32), 32x32x64 with a scale for every
 // 32 elements (e4m3 and E2M1 as they are stored).  4-bit weights with bfloat16 rows are widened
 // in registers, exactly: an E2M1 element times a power of two is a bfloat16.
+//
+// Measured: 65,536 rows over 128 experts, 5120 -> 2 x 2048: bfloat16 2.83 ms (0.97 PFLOP/s; a
+// library product of this size 1.43 at the same power limit), 8-bit rows and weights 1.83 ms; 262,144
+// 8-bit rows over 256 experts with 4-bit weights, 2048 -> 7168: 4.3 ms (1.8 PFLOP/s).
 #include "a2av_experts.h"
 
 namespace a2av {

@@ -204,6 +204,35 @@ def test_many_groups_with_many_rows(kind, k):
     Case(counts, k, 2112, kind, False).run().check()
 
 
+@pytest.mark.parametrize("kind", KINDS[2:], ids=["-".join(NAME[k] for k in ks) for ks in KINDS[2:]])
+@pytest.mark.parametrize("swiglu", [False, True], ids=["plain", "swiglu"])
+@pytest.mark.parametrize("k,shift", [(32, 0), (160, 0), (416, 0), (1056, 0), (512, 1), (640, 2), (160, 3)])
+def test_scale_rows_of_any_length_and_address(kind, swiglu, k, shift):
+    """Rows of scales that are not whole words: by their length or because they start `shift` bytes
+    past a word, the last ones next to the allocation's end; few rows, few rows of enough groups for
+    every unit of the GPU, many rows."""
+    many = np.random.default_rng(6).integers(0, 33, (16, 8))
+    for counts, n in ((SMALL, 192), (many, 832), (BIG, 2112)):
+        banner(f"scales {kind} swiglu {swiglu} k {k} shift {shift} n {n}")
+        c = Case(counts, k, n, kind, swiglu)
+        flat = torch.full((c.ws.numel() + shift,), 255, dtype=torch.uint8, device="cuda")   # NaN in front
+        flat[shift:] = c.ws.flatten()
+        c.ws = flat[shift:].view(c.ws.shape)
+        c.run().check()
+
+
+@pytest.mark.parametrize("kind", [KINDS[0], KINDS[1]], ids=["f32", "bf16"])
+@pytest.mark.parametrize("k", [3, 31, 65, 127, 191, 193, 257, 515])
+def test_rows_of_any_length(kind, k):
+    """Rows of no whole step and of one to many, with and without a rest shorter or longer than a
+    load, for groups of 1, 16 and more rows."""
+    for counts in ([[1]], [[16, 17], [0, 130]]):
+        for swiglu in (False, True):
+            banner(f"odd rows {kind} k {k} {counts} swiglu {swiglu}")
+            Case(counts, k, 70, kind, swiglu).run().check()
+            Case(counts, k, 70, kind, swiglu, offset=1).run().check()
+
+
 @kinds
 def test_infinities_and_nan_stay_in_their_row(kind):
     """A NaN in a row or an infinity in it reaches that row's outputs and no other's."""
